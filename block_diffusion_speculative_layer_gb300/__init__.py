@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Iterable, List, Optional, Sequence, Tuple, Union
+from typing import Any, Dict, Iterable, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import numpy as np
 
@@ -31,6 +31,7 @@ EXPORTED = [
     "df_generate_sampled", "df_philox4x32_10", "df_op_philox_uniforms", "df_op_sampling_probs",
     "df_op_sample_draw", "df_op_accept_sampled", "df_set_block_range", "df_block_size_for",
     "df_generate_accept_hist", "df_debug_wait_probe", "df_op_attention_bf16",
+    "df_op_kv8_write", "df_op_kv8_read", "df_op_attention_kv8",
 ]
 
 
@@ -130,6 +131,11 @@ def lib() -> ctypes.CDLL:
     L.df_generate_accept_hist.argtypes = [_P, _I, ctypes.POINTER(ctypes.c_int64)]
     L.df_debug_wait_probe.argtypes = [_P]
     L.df_op_attention_bf16.argtypes = [_P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P]
+    _L = ctypes.c_int64
+    L.df_op_kv8_write.argtypes = [_P, _P, _I, _I, _L, _L, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _P, _P]
+    L.df_op_kv8_read.argtypes = [_P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P]
+    L.df_op_attention_kv8.argtypes = [_P, _L, _P, _L, _P, _I, _I, _P, _P, _I, _I, _I, _I, _P, _I, _P, _P, _I, _I, _I,
+                                      _F, _I, _I, _I, _P, _P]
     L.df_block_size_for.argtypes = [ctypes.c_double, _I, _I]
     L.df_block_size_for.restype = _I
     for name in EXPORTED:
@@ -569,3 +575,170 @@ def block_size_for(tokens_per_cycle: float, b_min: int, b_max: int) -> int:
     if b < 0:
         raise DfError(DF_EINVAL, "df_block_size_for: bad arguments")
     return b
+
+
+# ------------------------------------------------------------------ 8-bit paged key/value cache
+class KV8Cache(NamedTuple):
+    """One layer's 8-bit paged cache (the format is described in dflash.h).
+    codes: [n_pages, 2, Hkv, page_tokens, head_dim] uint8 (the value plane's
+    bytes lie transposed in groups of 16 tokens); exps: [n_pages, Hkv,
+    page_tokens, 2] uint8; err: int32 word of the sticky error bits."""
+    codes: Any
+    exps: Any
+    err: Any
+
+
+def kv8_cache(n_pages: int, n_kv_heads: int, head_dim: int = 128, page_tokens: int = 16, device="cuda") -> KV8Cache:
+    """A cache of n_pages pages; every vector starts as zeros."""
+    import torch
+    if n_pages < 1 or n_kv_heads < 1 or head_dim not in (64, 128) or page_tokens % 16 or not 16 <= page_tokens <= 1024:
+        raise DfError(DF_EINVAL, "kv8_cache: head_dim 64 or 128, page_tokens a multiple of 16 up to 1024")
+    return KV8Cache(torch.zeros((n_pages, 2, n_kv_heads, page_tokens, head_dim), dtype=torch.uint8, device=device),
+                    torch.full((n_pages, n_kv_heads, page_tokens, 2), 127, dtype=torch.uint8, device=device),
+                    torch.zeros(1, dtype=torch.int32, device=device))
+
+
+def kv8_check(cache: KV8Cache):
+    """Raise if a call on this cache met a page id or length out of range
+    (or a wait that ran out), and clear its error word.  Synchronises."""
+    e = int(cache.err.item())
+    cache.err.zero_()
+    if e:
+        raise DfError(DF_ETIMEOUT if e & 1 else DF_EINVAL, f"kv8: device error bits {e}")
+
+
+_I32_MAX = 2 ** 31 - 1
+
+
+def _kv8_refuse(why: str):
+    raise DfError(DF_EINVAL, "kv8: " + why)
+
+
+def _kv8_plan(cache: KV8Cache, page_table, row_start, kv_len):
+    """Check the arguments every call shares; (device index, geometry)."""
+    import torch
+    codes, exps, err = cache
+    dev = codes.get_device()
+    if dev < 0:
+        _kv8_refuse("the cache must be on a CUDA device")
+    for t in (exps, err, page_table, row_start, kv_len):
+        if t.get_device() != dev:
+            _kv8_refuse("every tensor must be on the cache's device")
+    if codes.dtype != torch.uint8 or exps.dtype != torch.uint8 or err.dtype != torch.int32:
+        _kv8_refuse("codes and exps must be uint8, err int32")
+    if codes.dim() != 5 or codes.shape[1] != 2 or not codes.is_contiguous() or not exps.is_contiguous():
+        _kv8_refuse("codes must be a contiguous [n_pages, 2, heads, page_tokens, head_dim] tensor")
+    n, _, heads, page, hd = codes.shape
+    if exps.shape != (n, heads, page, 2) or err.numel() < 1:
+        _kv8_refuse("exps must be [n_pages, heads, page_tokens, 2]")
+    if page_table.dtype != torch.int32 or row_start.dtype != torch.int32 or kv_len.dtype != torch.int32:
+        _kv8_refuse("page_table, row_start and kv_len must be int32")
+    nseq = kv_len.shape[0]
+    if page_table.dim() != 2 or kv_len.dim() != 1 or row_start.shape != (nseq + 1,) or page_table.shape[0] < nseq:
+        _kv8_refuse("page_table [seqs, entries], row_start [seqs + 1] and kv_len [seqs] do not agree")
+    if not (page_table.is_contiguous() and row_start.is_contiguous() and kv_len.is_contiguous()):
+        _kv8_refuse("page_table, row_start and kv_len must be contiguous")
+    return dev, (n, page, heads, hd), nseq
+
+
+def _kv8_call(dev: int, stream, what: str, fn, *args):
+    """fn(*args, stream) on device `dev`'s current stream, or on `stream`."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device_index != dev:
+        _kv8_refuse("the stream belongs to another device")
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != DF_OK:
+        raise DfError(st, what)
+
+
+def _kv8_empty(shape, dtype, dev: int, stream):
+    """An output tensor that belongs to the stream the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
+def kv8_write(cache: KV8Cache, k, v, page_table, row_start, kv_len, stream=None):
+    """Quantise rows of keys and values into the cache (df_op_kv8_write).
+    k, v: [rows, Hkv, head_dim], bf16 or fp32, any row stride (a slice of a
+    fused projection); page_table [seqs, entries], row_start [seqs + 1],
+    kv_len [seqs] int32: sequence s owns rows row_start[s]..row_start[s + 1] - 1,
+    its last positions up to kv_len[s] - 1."""
+    import torch
+    dev, (n, page, heads, hd), nseq = _kv8_plan(cache, page_table, row_start, kv_len)
+    if k.get_device() != dev or v.get_device() != dev or k.dtype != v.dtype:
+        _kv8_refuse("k and v must be of one type, on the cache's device")
+    dt = DF_BF16 if k.dtype == torch.bfloat16 else DF_FP32 if k.dtype == torch.float32 else -1
+    if dt < 0 or k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (heads, hd):
+        _kv8_refuse("k and v must be bf16 or fp32 [rows, heads, head_dim]")
+    (ks, kh, kd), (vs, vh, vd) = k.stride(), v.stride()
+    rows = k.shape[0]
+    if rows and ((kh, kd) != (hd, 1) and heads > 1 or (vh, vd) != (hd, 1) and heads > 1 or kd != 1 or vd != 1):
+        _kv8_refuse("the heads of a row must be contiguous")
+    if rows < 2:  # a single row's stride says nothing
+        ks = vs = heads * hd
+    _kv8_call(dev, stream, "df_op_kv8_write", lib().df_op_kv8_write, k.data_ptr(), v.data_ptr(), dt, rows, ks, vs,
+              cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(),
+              page_table.shape[1], row_start.data_ptr(), kv_len.data_ptr(), nseq, cache.err.data_ptr())
+
+
+def kv8_read(cache: KV8Cache, page_table, row_start, kv_len, rows: int, dtype=None, k=None, v=None, stream=None):
+    """Read rows back (df_op_kv8_read): (k, v), each [rows, Hkv, head_dim] in
+    `dtype` (bf16, the default, or fp32).  k and v may be given."""
+    import torch
+    dev, (n, page, heads, hd), nseq = _kv8_plan(cache, page_table, row_start, kv_len)
+    dtype = dtype if dtype is not None else k.dtype if k is not None else torch.bfloat16
+    dt = DF_BF16 if dtype == torch.bfloat16 else DF_FP32 if dtype == torch.float32 else -1
+    if dt < 0 or rows < 0:
+        _kv8_refuse("rows must not be negative, and the type bf16 or fp32")
+    k = _kv8_empty((rows, heads, hd), dtype, dev, stream) if k is None else k
+    v = _kv8_empty((rows, heads, hd), dtype, dev, stream) if v is None else v
+    for t in (k, v):
+        if t.get_device() != dev or t.dtype != dtype or t.shape != (rows, heads, hd) or not t.is_contiguous():
+            _kv8_refuse("k and v must be contiguous [rows, heads, head_dim] tensors of the type")
+    _kv8_call(dev, stream, "df_op_kv8_read", lib().df_op_kv8_read, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
+              page, heads, hd, page_table.data_ptr(), page_table.shape[1], row_start.data_ptr(), kv_len.data_ptr(),
+              nseq, rows, dt, k.data_ptr(), v.data_ptr(), cache.err.data_ptr())
+    return k, v
+
+
+def attention_kv8(q, cache: KV8Cache, page_table, row_start, kv_len, max_rows: int, max_len: int, causal: bool = True,
+                  window: int = 0, scale: Optional[float] = None, out=None, lse=None, cluster_ctas: int = 0,
+                  stream=None):
+    """Attention of a chunk of new tokens over the cache (df_op_attention_kv8).
+    q: [rows, Hq * head_dim] bf16, any row stride; max_rows and max_len bound a
+    sequence's rows and kv_len; causal: a row sees positions up to its own
+    (the last `window` of them if window > 0), else every cached position of
+    its sequence; lse: fp32 [rows, Hq], filled if given, or True to make one.
+    Returns (out, lse)."""
+    import torch
+    dev, (n, page, heads, hd), nseq = _kv8_plan(cache, page_table, row_start, kv_len)
+    if q.get_device() != dev or q.dtype != torch.bfloat16 or q.dim() != 2 or q.shape[1] % hd:
+        _kv8_refuse("q must be bf16 [rows, Hq * head_dim] on the cache's device")
+    rows, width = q.shape
+    hq = width // hd
+    out = _kv8_empty((rows, width), torch.bfloat16, dev, stream) if out is None else out
+    if out.get_device() != dev or out.dtype != torch.bfloat16 or out.shape != (rows, width):
+        _kv8_refuse("out must be bf16 and shaped as q")
+    qs, os_ = (q.stride(0), out.stride(0)) if rows > 1 else (width, width)
+    if rows and (q.stride(1) != 1 or out.stride(1) != 1):
+        _kv8_refuse("the elements of a row must be contiguous")
+    if lse is True:
+        lse = _kv8_empty((rows, hq), torch.float32, dev, stream)
+    if lse is not None and (lse.get_device() != dev or lse.dtype != torch.float32 or lse.shape != (rows, hq) or
+                            not lse.is_contiguous()):
+        _kv8_refuse("lse must be a contiguous fp32 [rows, Hq] tensor")
+    _kv8_call(dev, stream, "df_op_attention_kv8", lib().df_op_attention_kv8, q.data_ptr(), qs, out.data_ptr(), os_,
+              lse.data_ptr() if lse is not None else None, rows, hq, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
+              page, heads, hd, page_table.data_ptr(), page_table.shape[1], row_start.data_ptr(), kv_len.data_ptr(),
+              nseq, min(int(max_rows), rows), min(int(max_len), _I32_MAX), scale if scale is not None else hd ** -0.5,
+              1 if causal else 0, min(int(window), _I32_MAX), cluster_ctas, cache.err.data_ptr())
+    return out, lse

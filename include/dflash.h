@@ -505,6 +505,96 @@ df_status df_op_accept_sampled(const int32_t* drafts_dev, const float* q_logits_
                                const float* u_dev, int32_t* k_dev, int32_t* tok_dev, int32_t* err_dev,
                                void* stream);
 
+/* ---- 8-bit paged key/value cache ------------------------------------------
+ * A paged cache that holds keys and values as e4m3 codes with one power-of-
+ * two scale per vector (one token, one head, key or value), the calls that
+ * write rows into it and read rows back, and the attention of a chunk of new
+ * tokens over it.  It halves what a verify pass reads of a bf16 cache; for
+ * callers with their own loop, on caller-owned device buffers.
+ *
+ * Format.  A vector x of head_dim elements is stored as codes c_d and an
+ * exponent byte b, and stands for c_d * 2^(b - 127): b - 127 is the smallest
+ * integer e in [-100, 119] with max|x_d| <= 448 * 2^e (larger magnitudes
+ * saturate), and c_d is x_d * 2^-e rounded to e4m3, to nearest, ties to even.
+ * A vector with an infinity or a NaN is stored as b = 255 and zero codes and
+ * reads back as NaN.
+ *   codes_dev [n_pages][k|v][n_kv_heads][page_tokens * head_dim] bytes, a
+ *     page-head's keys token by token ([page_tokens][head_dim]) and its values
+ *     transposed in groups of 16 tokens ([page_tokens / 16][head_dim][16])
+ *   exps_dev  [n_pages][n_kv_heads][page_tokens][k|v] bytes
+ * page_tokens: a multiple of 16, at most 1024; head_dim: 64 or 128.
+ *
+ * Rows.  A call works on the rows of nseq sequences, packed back to back:
+ * sequence s owns rows row_start[s] .. row_start[s + 1] - 1, and they are its
+ * last positions: row j of its n rows is position kv_len[s] - n + j.  Rows at
+ * negative positions are padding (the start of a left-padded batch): writing
+ * skips them, reading gives zeros, attention gives a zero row.  Rows outside
+ * [row_start[0], row_start[nseq]) are left as they are.
+ *   row_start_dev  [nseq + 1] int32, ascending, within [0, rows]
+ *   kv_len_dev     [nseq] int32: the sequence's cached positions, these rows included
+ *   page_table_dev [nseq][pt_stride] int32: page ids of positions 0,
+ *                  page_tokens, 2 * page_tokens, ...
+ * All three are read on the device, so a captured graph may be replayed with
+ * other lengths.  A sequence whose entries are out of range (row_start, or a
+ * kv_len outside [0, pt_stride * page_tokens]) is left out, and a page id
+ * outside [0, n_pages) makes its positions unwritten, zero when read and
+ * invisible to attention; both set bit 2 of err_dev.
+ *
+ * Every call is stream-ordered, allocates nothing, keeps nothing between
+ * calls, does not synchronise and can be captured.  err_dev (may be NULL): a
+ * device int that receives sticky error bits (1: a bounded wait ran out, 2: an
+ * index out of range).  Arrays are 16-byte aligned (the int32 ones 4).  rows
+ * or nseq 0: nothing to do, DF_OK. */
+
+/* Quantise rows of keys and values and write them into the cache.  k_dev and
+ * v_dev: [rows][n_kv_heads][head_dim] in `dtype` (DF_FP32 or DF_BF16), with
+ * k_stride / v_stride elements from row to row (the heads of a row are
+ * contiguous; a stride is a multiple of 16 bytes).  A page that two sequences
+ * of a call write at the same position receives either's bytes: give shared
+ * pages to one of them. */
+df_status df_op_kv8_write(const void* k_dev, const void* v_dev, int32_t dtype, int32_t rows, int64_t k_stride,
+                          int64_t v_stride, void* codes_dev, void* exps_dev, int32_t n_pages, int32_t page_tokens,
+                          int32_t n_kv_heads, int32_t head_dim, const int32_t* page_table_dev, int32_t pt_stride,
+                          const int32_t* row_start_dev, const int32_t* kv_len_dev, int32_t nseq, int32_t* err_dev,
+                          void* stream);
+
+/* Read rows back: k_dev and v_dev [rows][n_kv_heads][head_dim] in `dtype`,
+ * contiguous.  The values c_d * 2^(b - 127), exact in both types. */
+df_status df_op_kv8_read(const void* codes_dev, const void* exps_dev, int32_t n_pages, int32_t page_tokens,
+                         int32_t n_kv_heads, int32_t head_dim, const int32_t* page_table_dev, int32_t pt_stride,
+                         const int32_t* row_start_dev, const int32_t* kv_len_dev, int32_t nseq, int32_t rows,
+                         int32_t dtype, void* k_dev, void* v_dev, int32_t* err_dev, void* stream);
+
+/* Attention of the rows over their sequences' cached positions (the rows' own
+ * keys and values written before):
+ *   out[r] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q[r] . k_t),
+ * over the positions t that row r (at position p) sees: 0..p (causal = 1),
+ * p - window + 1..p (causal = 1, window > 0), or 0..kv_len - 1 (causal = 0:
+ * a drafter's block, which sees its context and itself whole; [ARCH] 第三层
+ * Block Diffusion).  bf16 queries and outputs, fp32 softmax and accumulation.
+ *   q_dev, out_dev  [rows][n_q_heads][head_dim] bf16, q_stride / out_stride
+ *                   elements from row to row (multiples of 8); n_q_heads a
+ *                   multiple of n_kv_heads, query head h reads KV head
+ *                   h / (n_q_heads / n_kv_heads)
+ *   lse_dev         NULL, or fp32 [rows][n_q_heads]: ln sum_t p_t, for joining
+ *                   attentions over parts of the keys
+ *   scale           finite, e.g. 1 / sqrt(head_dim)
+ *   max_rows        bound on one sequence's rows (a longer one is left out and
+ *                   sets error bit 2)
+ *   max_len         bound on kv_len, used to choose the split alone
+ *   cluster_ctas    CTAs that share one tile's keys: 1, 2, 4, 8 or 16, or 0
+ *                   for a choice by the sizes.  The split decides the order of
+ *                   summation: a row's bits depend on its own query and keys
+ *                   and on this number, not on the other rows of the call.
+ * A row that sees nothing gives zeros and lse -inf; a row that sees a vector
+ * without numbers (byte 255) gives NaN. */
+df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev, int64_t out_stride, float* lse_dev,
+                              int32_t rows, int32_t n_q_heads, const void* codes_dev, const void* exps_dev,
+                              int32_t n_pages, int32_t page_tokens, int32_t n_kv_heads, int32_t head_dim,
+                              const int32_t* page_table_dev, int32_t pt_stride, const int32_t* row_start_dev,
+                              const int32_t* kv_len_dev, int32_t nseq, int32_t max_rows, int32_t max_len, float scale,
+                              int32_t causal, int32_t window, int32_t cluster_ctas, int32_t* err_dev, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
