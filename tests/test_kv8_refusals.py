@@ -72,7 +72,7 @@ def test_bad_attention(dfl):
     for bad in (dict(q=None), dict(out=None), dict(hq=36), dict(hq=4), dict(hq=0), dict(qs=4088), dict(os=4092),
                 dict(qs=4100), dict(q=P(0x1008)), dict(out=P(0x1002)), dict(lse=P(0x1002)), dict(max_rows=-1),
                 dict(max_len=-1), dict(causal=2), dict(window=-1), dict(window=5, causal=0), dict(scale=math.nan),
-                dict(scale=math.inf), dict(cla=3), dict(cla=32), dict(cla=-1), dict(nseq=1 << 17)):
+                dict(scale=math.inf), dict(cla=3), dict(cla=32), dict(cla=-1), dict(nseq=1 << 21)):
         assert attend(dfl, **bad) == dfl.DF_EINVAL, bad
     assert attend(dfl, max_rows=0) == dfl.DF_OK
 
