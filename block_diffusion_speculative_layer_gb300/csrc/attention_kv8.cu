@@ -4,18 +4,23 @@
 // A tile is up to N (16, 32 or 64) query rows of one sequence and KV head:
 // row r of the tile is query token r / G, head r % G of the group.  The keys
 // come in chunks of 128 positions.  Per chunk
-//   S^T [128 keys][N]   = K [128][hd] . Q^T            A = K,   B = Q
-//   P^T                 = 2^(s c_t + e_t - M_r)
-//   O^T [hd][N]        += V^T [hd][128] . P^T          A = V^T, B = P^T
+//   S^T [128 keys][N]  = K [128][hd] . (Qhi + Qlo)^T   A = K (e4m3, as cached)
+//   P^T                = 2^(s c_t + e_t - M_r)
+//   O^T [hd][N]       += V^T [hd][128] . P^T           A = V^T (f16), B = P^T (f16)
 // with keys (and head dims) on the tensor core's 128 lanes and query rows on
 // its columns.  That way round a thread holds one key of S, so the key's and
 // the value's power-of-two scale is one number per thread (c_t = 2^(b_k - 127)
-// scale log2 e, and e_t = b_v - 127 added to the exponent), and both codes
-// reach the tensor core as A operands through tensor memory: each thread
-// widens its key's codes (its head dim's codes of 128 values: the cache keeps
-// values transposed) to f16, exactly, and stores them to its own lane.  No
-// widened tile passes through shared memory, and the cache's 8-bit bytes are
-// all that is staged there.
+// scale log2 e, and e_t = b_v - 127 added to the exponent).
+//
+// Keys go from the cache's bytes to the tensor core without a conversion: a
+// bf16 query has 8 bits, so a row brought to a largest magnitude in [128, 256)
+// by a power of two f_r is the sum of two e4m3 numbers of 4 bits each, exactly
+// for elements down to 2^-9 of the largest and to within 2^-17 of it below.
+// Both products go to one accumulator; the scores are taken times f_r.
+// Values need P at more than 8 bits and a wide range, so their product is f16:
+// a thread widens its head dim's codes of 128 values (the cache keeps values
+// transposed), exactly, and stores them to its own lane of tensor memory, the
+// A operand.  No widened tile passes through shared memory.
 //
 // Softmax: M_r bounds (up to 2^8) the size s c_t + e_t of the terms that
 // enter the product, so P fits f16 whatever the values' scales.  It moves
@@ -30,10 +35,12 @@
 // The CTAs of a cluster take every C-th chunk of a tile and add their parts
 // through distributed shared memory in rank order.
 //
-// Roles (160 threads): warps 0-3 widen, run the softmax and (thread 0) issue
-// the tensor-core instructions; warp 4 stages keys, values and exponents by
-// TMA in two stages each, and owns the tensor memory.  Two CTAs fit on an SM
-// (256 columns and less than 113 KB each) and fill each other's waits.
+// Roles (192 threads): warps 0-3 widen values and run the softmax; warp 4
+// stages keys, values and exponents by TMA in two stages each; warp 5 issues
+// the tensor-core instructions and owns the tensor memory.  S leaves tensor
+// memory for registers at once, so the next chunk's S is computed while the
+// softmax of this one runs.  Two CTAs fit on an SM (256 columns and less than
+// 113 KB each) and fill each other's waits.
 //
 // Every wait is bounded (about two seconds).  A thread whose wait ran out
 // flags it and goes on without waiting, so all threads reach every barrier.
@@ -58,7 +65,7 @@ struct Kv8Attn {
 
 constexpr int K8_CHUNK = 128;     // keys per chunk: one per tensor-memory lane
 constexpr int K8_STAGES = 2;
-constexpr int K8_THREADS = 160;
+constexpr int K8_THREADS = 192;
 constexpr int K8_SMS = 152;
 constexpr int K8_COLS = 256;      // tensor-memory columns of a CTA
 constexpr float K8_SLACK = 8.f;   // how far (log2) a term may pass M before M moves
@@ -71,8 +78,8 @@ struct K8Smem {
   static constexpr int TILE = K8_CHUNK * HD;            // one stage of key (or value) codes
   static constexpr int K = 0;
   static constexpr int V = K + K8_STAGES * TILE;
-  static constexpr int Q = V + K8_STAGES * TILE;        // [hd / 64][N rows][128 B] f16, 128-byte swizzle
-  static constexpr int P = Q + (HD / 64) * N * 128;     // [128 keys][128 B], row r at f16 column r, 128-byte swizzle
+  static constexpr int Q = V + K8_STAGES * TILE;        // [hi, lo][N rows][HD] e4m3, swizzled as the keys
+  static constexpr int P = Q + 2 * N * HD;              // [128 keys][128 B], row r at f16 column r, 128-byte swizzle
   static constexpr int E = P + K8_CHUNK * 128;          // exponent bytes: [stage][128 keys][k|v]
   static constexpr int END = E + K8_STAGES * K8_CHUNK * 2;
   static constexpr int BYTES = END + 1024;
@@ -147,18 +154,29 @@ __device__ __forceinline__ void k8_load_bytes(uint32_t dst, const void* src, uin
                : "memory");
 }
 
-// Shared-memory descriptor of a B operand in the 128-byte swizzle, 8-row
-// groups 1024 bytes apart.  Q: K-major (rows = query rows).  P: MN-major
-// (rows = keys, query rows along a 128-byte row).
+// Shared-memory descriptors.  Rows of 128 bytes in the 128-byte swizzle (8-row
+// groups 1024 bytes apart) or of 64 bytes in the 64-byte swizzle (512 bytes
+// apart).  K and Q: K-major.  P: MN-major (rows = keys, query rows along a row).
+template <int ROW>
 __device__ __forceinline__ uint64_t k8_desc(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+  static_assert(ROW == 128 || ROW == 64, "row bytes");
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)((8 * ROW) >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)(ROW == 128 ? 2 : 4) << 61);
 }
-// Instruction descriptor of kind::f16: f16 A and B, fp32 accumulator, 128 x N.
+// Instruction descriptor: A and B f16 (kind::f16) or e4m3 (kind::f8f6f4), fp32 accumulator, 128 x N.
 __host__ __device__ constexpr uint32_t k8_idesc(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-// D += A . B with A in tensor memory.
+// D = (acc) D + A . B, e4m3, both in shared memory.
+__device__ __forceinline__ void k8_mma_codes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// D = (acc) D + A . B, f16, A in tensor memory.
 __device__ __forceinline__ void k8_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -172,27 +190,17 @@ __device__ __forceinline__ void k8_commit(uint32_t bar) {
 }
 
 // 16 columns of the thread's tensor-memory lane.  The load's registers are
-// valid once k8_ld_wait has passed them through.
+// valid once k8_ld_wait16 has passed them through.
 __device__ __forceinline__ void k8_ld16(uint32_t addr, float* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-      : "r"(addr));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+               : "r"(addr));
 }
 __device__ __forceinline__ void k8_ld_wait16(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
-}
-template <int N>
-__device__ __forceinline__ void k8_ld(uint32_t addr, float* v) {
-#pragma unroll
-  for (int i = 0; i < N; i += 16) k8_ld16(addr + i, v + i);
-#pragma unroll
-  for (int i = 0; i < N; i += 16) k8_ld_wait16(v + i);
 }
 __device__ __forceinline__ void k8_st16(uint32_t addr, const uint32_t* v) {
   asm volatile(
@@ -231,6 +239,11 @@ __device__ __forceinline__ uint64_t k8_mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ float k8_ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float k8_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // Largest value over the warp (numbers win over NaN).
@@ -287,18 +300,17 @@ template <int HD, int N>
 __global__ void __launch_bounds__(K8_THREADS, 2)
     kv8_attention_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap kmap) {
   using L = K8Smem<HD, N>;
-  constexpr int KCOLS = HD / 2;              // tensor-memory columns: widened keys,
-  constexpr int VCOL = KCOLS;                // widened values (128 keys, two to a column),
-  constexpr int SCOL = KCOLS + 64;           // S,
+  constexpr int VCOL = 0;                    // tensor-memory columns: widened values (128 keys, two to a
+  constexpr int SCOL = 128;                  // column) of an even and an odd chunk, S,
   constexpr int OCOL = SCOL + N;             // O
   static_assert(OCOL + N <= K8_COLS, "tensor-memory columns");
   extern __shared__ __align__(128) uint8_t k8_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(k8_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t s_fk[K8_STAGES], s_fv[K8_STAGES], s_ek[K8_STAGES], s_ev[K8_STAGES], s_s, s_o;
+  __shared__ __align__(8) uint64_t s_fk[K8_STAGES], s_fv[K8_STAGES], s_ek[K8_STAGES], s_ev[K8_STAGES], s_s, s_r, s_p, s_o;
   __shared__ uint32_t s_tmem;
   __shared__ int s_live[K8_STAGES];                        // groups of the chunk that hold positions
   __shared__ __align__(16) float s_m[N], s_neg[N], s_fac[N], s_qf[N], s_l[N];
-  __shared__ __align__(16) int s_lo[N], s_hi[N];
+  __shared__ __align__(16) int s_lo[N], s_hi[N], s_tok[N], s_hd[N];  // what a row sees; its token and query head
   __shared__ float s_red[4][N];
 
   const Kv8Geom& g = a.g;
@@ -322,7 +334,9 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
   for (int r = threadIdx.x; r < N; r += K8_THREADS) {
     int lo = 0x7fffffff, hi = -1;
     if (r < nr) {
-      const int pos = sq.pos0 + (r0 + r) / G;
+      const int j = (r0 + r) / G, pos = sq.pos0 + j;
+      s_tok[r] = sq.row0 + j;
+      s_hd[r] = head * G + (r0 + r) - j * G;
       lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
       hi = pos < 0 ? -1 : a.causal ? pos : len - 1;
     }
@@ -335,15 +349,17 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
     for (int i = 0; i < K8_STAGES; ++i) {
       k8_bar_init(k8_addr(&s_fk[i]), 1);
       k8_bar_init(k8_addr(&s_fv[i]), 1);
-      k8_bar_init(k8_addr(&s_ek[i]), 4);
+      k8_bar_init(k8_addr(&s_ek[i]), 1);
       k8_bar_init(k8_addr(&s_ev[i]), 4);
     }
-    k8_bar_init(k8_addr(&s_s), 1);
-    k8_bar_init(k8_addr(&s_o), 1);
+    k8_bar_init(k8_addr(&s_s), 1);  // S computed
+    k8_bar_init(k8_addr(&s_r), 4);  // S read, one arrival per softmax warp
+    k8_bar_init(k8_addr(&s_p), 4);  // V^T and P written
+    k8_bar_init(k8_addr(&s_o), 1);  // O updated
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
   }
-  if (warp == 4) {
+  if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(k8_addr(&s_tmem)),
                  "n"(K8_COLS)
                  : "memory");
@@ -365,13 +381,13 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
   bool ok = true;
   if (warp == 4) {
     // ============================================================== producer
-    // lanes 0-7 bring a chunk's groups of 16 keys with their exponents, lanes 8-15 its groups of values
+    // lanes 0-7 bring a chunk's groups of 16 keys, lanes 8-15 its groups of values, lanes 16-23 the exponents
     const int gr = lane & 7;
     for (int i = 0; i < n_mine; ++i) {
       const int st = i % K8_STAGES, c = c_first + i * C;
       const int pos = c * K8_CHUNK + gr * 16;
       int page = -1;
-      if (lane < 16 && pos < len) {
+      if (lane < 24 && pos < len) {
         page = g.page_table[(size_t)s * g.pt_stride + pos / g.page_tokens];
         if (page < 0 || page >= g.n_pages) {
           page = -1;
@@ -386,29 +402,31 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
       }
       const int slot = pos % g.page_tokens;
       if (lane == 0) {
-        s_live[st] = (int)live;
-        k8_arrive_tx(k8_addr(&s_fk[st]), __popc(live) * (16 * HD + 32));
+        k8_arrive_tx(k8_addr(&s_fk[st]), __popc(live) * 16 * HD);
       }
       __syncwarp();
-      if (lane < 8 && page >= 0) {
+      if (lane < 8 && page >= 0)
         k8_load_keys(k8_addr(sm + L::K + st * L::TILE + gr * 16 * HD), &kmap, k8_addr(&s_fk[st]), slot,
                      (page * 2) * g.heads + head);
-        k8_load_bytes(k8_addr(sm + L::E + st * K8_CHUNK * 2 + gr * 32), g.exps + kv8_exp_at(g, page, head, slot), 32,
-                      k8_addr(&s_fk[st]));
-      }
       if (i >= K8_STAGES) {
         k8_wait(k8_addr(&s_ev[st]), (uint32_t)(i / K8_STAGES - 1) & 1u, ok, g.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
-      if (lane == 0) k8_arrive_tx(k8_addr(&s_fv[st]), __popc(live) * 16 * HD);
+      if (lane == 0) {
+        s_live[st] = (int)live;
+        k8_arrive_tx(k8_addr(&s_fv[st]), __popc(live) * (16 * HD + 32));
+      }
       __syncwarp();
-      if (lane >= 8 && page >= 0)
+      if (lane >= 16 && page >= 0)
+        k8_load_bytes(k8_addr(sm + L::E + st * K8_CHUNK * 2 + gr * 32), g.exps + kv8_exp_at(g, page, head, slot), 32,
+                      k8_addr(&s_fv[st]));
+      if (lane >= 8 && lane < 16 && page >= 0)
         k8_load_bytes(k8_addr(sm + L::V + st * L::TILE + gr * 16 * HD),
                       g.codes + kv8_code_at(g, page, 1, head) + (size_t)slot * HD, 16 * HD, k8_addr(&s_fv[st]));
     }
-    // The consumers wait for every tile, so no copy is in flight when they are
-    // done; if a wait ran out, give the copies issued the same time to land.
+    // The other warps wait for every tile, so no copy is in flight when they
+    // are done; if a wait ran out, give the copies issued the same time to land.
     if (!ok)
       for (int b = 0; b < K8_STAGES; ++b)
         for (uint32_t p = 0; p < 2; ++p) {
@@ -416,44 +434,102 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
           (void)(k8_test(k8_addr(&s_fv[b]), p) || k8_wait_slow(k8_addr(&s_fv[b]), p, g.err));
         }
     __syncwarp();
+  } else if (warp == 5) {
+    // ================================================================ issuer
+    asm volatile("bar.sync 3, 160;" ::: "memory");  // Q is in shared memory
+    if (lane == 0 && n_mine > 0) {
+      const uint64_t kd = k8_desc<HD>(k8_addr(sm + L::K)), qd = k8_desc<HD>(k8_addr(sm + L::Q)),
+                     pd = k8_desc<128>(k8_addr(sm + L::P));
+      // S^T of chunk i; its key tile is free when that is done
+      auto scores = [&](int i) {
+        const int st = i % K8_STAGES;
+        k8_wait(k8_addr(&s_fk[st]), (uint32_t)(i / K8_STAGES) & 1u, ok, g.err);
+        k8_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)  // the queries' high halves, then the low ones
+          k8_mma_codes(tmem + SCOL, kd + (uint64_t)((st * L::TILE + kk % (HD / 32) * 32) >> 4),
+                       qd + (uint64_t)((kk / (HD / 32) * N * HD + kk % (HD / 32) * 32) >> 4), k8_idesc(N, false),
+                       kk > 0);
+        k8_commit(k8_addr(&s_s));
+        k8_commit(k8_addr(&s_ek[st]));
+      };
+      scores(0);
+      for (int i = 0; i < n_mine; ++i) {
+        if (i + 1 < n_mine) {
+          k8_wait(k8_addr(&s_r), (uint32_t)i & 1u, ok, g.err);
+          scores(i + 1);
+        }
+        k8_wait(k8_addr(&s_p), (uint32_t)i & 1u, ok, g.err);
+        k8_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < K8_CHUNK / 16; ++kk)
+          k8_mma(tmem + OCOL, tmem + VCOL + (i & 1) * 64 + 8 * kk, pd + (uint64_t)((kk * 2048) >> 4), k8_idesc(N, true),
+                 i > 0 || kk > 0);
+        k8_commit(k8_addr(&s_o));
+      }
+      // every product has finished before tensor memory is freed
+      bool done = true;
+      k8_wait(k8_addr(&s_o), (uint32_t)(n_mine - 1) & 1u, done, g.err);
+    }
+    __syncwarp();
   } else {
-    // ==================================== widening, softmax, tensor-core issue
+    // ==================================================== widening, softmax
     const int t = threadIdx.x;  // tensor-memory lane: the chunk's key t, and head dim t
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
 
-    // Q as f16: exact unless a row holds a magnitude of 2^15 or more, which
-    // brings that row a power of two of its own (magnitudes below 2^-14 round
-    // to multiples of 2^-24).
-    constexpr int LPR = HD / 8;  // lanes per row, 8 elements each
-    bool scaled = false;
-    for (int r = t / LPR; r < N; r += 128 / LPR) {
-      const int sub = t % LPR;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (r < nr && s_hi[r] >= 0)
-        w = *reinterpret_cast<const uint4*>(a.q + (long long)(sq.row0 + (r0 + r) / G) * a.qs +
-                                            (size_t)(head * G + (r0 + r) % G) * HD + sub * 8);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-      uint32_t top = 0;
+    // Q as two e4m3 numbers
+    constexpr int LPR = HD / 8, RPP = 128 / LPR, QPASS = (N + RPP - 1) / RPP;  // lanes per row, rows per pass
+    const int sub = t % LPR;
+    {
+      uint4 qw[QPASS];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = max(top, max(ws[i] & 0x7FFFu, (ws[i] >> 16) & 0x7FFFu));
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int over = min(max((int)(top >> 7) - 127 - 14, 0), 113);  // exponent above 2^14
-      const float down = kv8_pow2(-over);
-      uint32_t h[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __half2 v = __floats2half2_rn(__uint_as_float(ws[i] << 16) * down,
-                                            __uint_as_float(ws[i] & 0xFFFF0000u) * down);
-        h[i] = *reinterpret_cast<const uint32_t*>(&v);
+      for (int i = 0; i < QPASS; ++i) {  // all loads first
+        const int r = t / LPR + i * RPP;
+        qw[i] = make_uint4(0, 0, 0, 0);
+        if (r < nr && s_hi[r] >= 0)
+          qw[i] = *reinterpret_cast<const uint4*>(a.q + s_tok[r] * a.qs + s_hd[r] * HD + sub * 8);
       }
-      *reinterpret_cast<uint4*>(sm + L::Q + (sub >> 3) * N * 128 + r * 128 + (((sub & 7) ^ (r & 7)) << 4)) =
-          make_uint4(h[0], h[1], h[2], h[3]);
-      if (sub == 0) s_qf[r] = kv8_pow2(over);
-      scaled = scaled || over > 0;
+#pragma unroll
+      for (int i = 0; i < QPASS; ++i) {
+        const int r = t / LPR + i * RPP;
+        const uint32_t ws[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) top = max(top, max(ws[u] & 0x7FFFu, (ws[u] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the power of two taken out of the row (a row that holds no numbers becomes NaN)
+        const int out = min(max((int)(top >> 7) - 127 - 7, -119), 120);
+        const float by = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : kv8_pow2(-out);
+        float x[8], hi[8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[2 * u] = __uint_as_float(ws[u] << 16) * by;
+          x[2 * u + 1] = __uint_as_float(ws[u] & 0xFFFF0000u) * by;
+        }
+        const uint2 ch = make_uint2(kv8_pack4(x[0], x[1], x[2], x[3]), kv8_pack4(x[4], x[5], x[6], x[7]));
+        const uint32_t two[4] = {ch.x & 0xFFFFu, ch.x >> 16, ch.y & 0xFFFFu, ch.y >> 16};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float2 f = kv8_value2(two[u]);
+          hi[2 * u] = f.x;
+          hi[2 * u + 1] = f.y;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] -= hi[u];
+        const uint2 cl = make_uint2(kv8_pack4(x[0], x[1], x[2], x[3]), kv8_pack4(x[4], x[5], x[6], x[7]));
+        if (r < N) {
+          const int piece = sub >> 1, at = HD == 128 ? (piece ^ (r & 7)) : (piece ^ ((r >> 1) & 3));
+          uint8_t* dst = sm + L::Q + r * HD + at * 16 + (sub & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = ch;
+          *reinterpret_cast<uint2*>(dst + N * HD) = cl;
+          if (sub == 0) s_qf[r] = kv8_pow2(out);
+        }
+      }
     }
     k8_fence_smem();
-    const bool any_scaled = k8_vote(scaled);
+    asm volatile("bar.arrive 3, 160;" ::: "memory");
+    k8_sync();
 
     // rows that exist: positions every one of them sees
     const int full_lo = s_lo[nr - 1], full_hi = s_hi[0];
@@ -463,98 +539,78 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
     if (HD < 128 && t >= HD) {  // lanes past the head dims add zeros to rows of O nobody reads
       const uint32_t z[16] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k8_st16(lane_base + VCOL + 16 * i, z);
+      for (int i = 0; i < 8; ++i) k8_st16(lane_base + VCOL + 16 * i, z);
     }
-
-    const uint64_t qd = k8_desc(k8_addr(sm + L::Q)), pd = k8_desc(k8_addr(sm + L::P));
-    float ct = 0.f, et = 0.f, ie = 1.f;
-    int live = 0;
     bool pending = true;  // some row has no term yet
 
-    // Chunk i's keys: exponents to registers, codes widened into this lane; then S^T = K Q^T.
-    auto keys = [&](int i) {
-      const int st = i % K8_STAGES;
-      k8_wait(k8_addr(&s_fk[st]), (uint32_t)(i / K8_STAGES) & 1u, ok, g.err);
-      live = s_live[st];
-      const uint32_t ee = *reinterpret_cast<const uint16_t*>(sm + L::E + st * K8_CHUNK * 2 + t * 2);
-      const uint8_t* row = sm + L::K + st * L::TILE + t * HD;
-      uint32_t w[KCOLS];
-#pragma unroll
-      for (int p = 0; p < HD / 16; ++p) {
-        const int at = HD == 128 ? (p ^ (t & 7)) : (p ^ ((t >> 1) & 3));
-        k8_widen16(*reinterpret_cast<const uint4*>(row + at * 16), w + 8 * p);
-      }
-      __syncwarp();
-      if (lane == 0) k8_arrive(k8_addr(&s_ek[st]));
-#pragma unroll
-      for (int p = 0; p < KCOLS / 16; ++p) k8_st16(lane_base + 16 * p, w + 16 * p);
-      const bool here = (live >> (t >> 4)) & 1;
-      const int bk = ee & 255, bv = ee >> 8;
-      ct = here ? kv8_scale(bk) * a.scale_log2 : 0.f;
-      et = !here ? 0.f : bv == KV8_NAN ? __uint_as_float(0x7FC00000u) : (float)(bv - KV8_BIAS);
-      ie = !here || bv == KV8_NAN ? 1.f : __uint_as_float((uint32_t)(254 - bv) << 23);
-      k8_st_wait();
-      k8_fence_before();
-      k8_sync();
-      if (t == 0) {
-        k8_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          k8_mma(tmem + SCOL, tmem + 8 * kk, qd + (uint64_t)(((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4),
-                 k8_idesc(N, false), kk > 0);
-        k8_commit(k8_addr(&s_s));
-      }
-    };
-
-    if (n_mine > 0) keys(0);
     for (int i = 0; i < n_mine; ++i) {
       const int st = i % K8_STAGES, key0 = (c_first + i * C) * K8_CHUNK;
-      // ---- values (V^T and P are read by the last chunk's product until it is done)
-      if (i > 0) k8_wait(k8_addr(&s_o), (uint32_t)(i - 1) & 1u, ok, g.err);
-      k8_fence_after();
+      // ---- this key's scales
       k8_wait(k8_addr(&s_fv[st]), (uint32_t)(i / K8_STAGES) & 1u, ok, g.err);
+      const int live = s_live[st];
+      const uint32_t ee = *reinterpret_cast<const uint16_t*>(sm + L::E + st * K8_CHUNK * 2 + t * 2);
+      const bool here = (live >> (t >> 4)) & 1;
+      const int bk = ee & 255, bv = ee >> 8;
+      const float ct = here ? kv8_scale(bk) * a.scale_log2 : 0.f;
+      const float et = !here ? 0.f : bv == KV8_NAN ? __uint_as_float(0x7FC00000u) : (float)(bv - KV8_BIAS);
+      const float ie = !here || bv == KV8_NAN ? 1.f : __uint_as_float((uint32_t)(254 - bv) << 23);
+      const uint64_t ct2 = k8_pair(ct, ct), et2 = k8_pair(et, et), ie2 = k8_pair(ie, ie);
+      const bool masked = live != 0xff || key0 < full_lo || key0 + K8_CHUNK - 1 > full_hi;
+      const int pos = here && key0 + t < len ? key0 + t : -1;
+
+      // ---- values (the product of two chunks ago has read this buffer: O's wait below)
       if (HD == 128 || t < HD) {
         const uint8_t* row = sm + L::V + st * L::TILE + t * 16;
         const bool tail = live != 0xff || key0 + K8_CHUNK > len;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t w[16];
+        for (int h = 0; h < 2; ++h) {
+          uint4 v[4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int gr = 2 * h + u;
-            uint4 v = *reinterpret_cast<const uint4*>(row + gr * 16 * HD);
-            if (tail) {  // bytes behind the last position may be anything: zeros
-              const int n = (live >> gr) & 1 ? len - key0 - gr * 16 : 0;
-              v.x = n >= 4 ? v.x : n <= 0 ? 0u : v.x & ((1u << (8 * n)) - 1);
-              v.y = n >= 8 ? v.y : n <= 4 ? 0u : v.y & ((1u << (8 * (n - 4))) - 1);
-              v.z = n >= 12 ? v.z : n <= 8 ? 0u : v.z & ((1u << (8 * (n - 8))) - 1);
-              v.w = n >= 16 ? v.w : n <= 12 ? 0u : v.w & ((1u << (8 * (n - 12))) - 1);
+          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(row + (4 * h + q) * 16 * HD);
+          if (tail) {  // bytes behind the last position may be anything: zeros
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int gr = 4 * h + q, n = (live >> gr) & 1 ? len - key0 - gr * 16 : 0;
+              v[q].x = n >= 4 ? v[q].x : n <= 0 ? 0u : v[q].x & ((1u << (8 * n)) - 1);
+              v[q].y = n >= 8 ? v[q].y : n <= 4 ? 0u : v[q].y & ((1u << (8 * (n - 4))) - 1);
+              v[q].z = n >= 12 ? v[q].z : n <= 8 ? 0u : v[q].z & ((1u << (8 * (n - 8))) - 1);
+              v[q].w = n >= 16 ? v[q].w : n <= 12 ? 0u : v[q].w & ((1u << (8 * (n - 12))) - 1);
             }
-            k8_widen16(v, w + 8 * u);
           }
-          k8_st16(lane_base + VCOL + 16 * h, w);
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            uint32_t w[16];
+            k8_widen16(v[q], w);
+            k8_widen16(v[q + 1], w + 8);
+            k8_st16(lane_base + VCOL + (i & 1) * 64 + 32 * h + 8 * q, w);
+          }
         }
       }
       __syncwarp();
       if (lane == 0) k8_arrive(k8_addr(&s_ev[st]));
 
-      // ---- softmax of key t's column of scores
+      // ---- its terms' exponents, straight from tensor memory
       k8_wait(k8_addr(&s_s), (uint32_t)i & 1u, ok, g.err);
       k8_fence_after();
-      const bool masked = live != 0xff || key0 < full_lo || key0 + K8_CHUNK - 1 > full_hi;
-      const int pos = ((live >> (t >> 4)) & 1) && key0 + t < len ? key0 + t : -1;
-      const uint64_t ct2 = k8_pair(ct, ct), et2 = k8_pair(et, et), ie2 = k8_pair(ie, ie);
       float y[N];
-      auto scores = [&] {
-        k8_ld<N>(lane_base + SCOL, y);
-        if (any_scaled)
+      for (bool again = false;; again = true) {
 #pragma unroll
-          for (int r = 0; r < N; ++r) y[r] *= s_qf[r];
+        for (int c0 = 0; c0 < N; c0 += 32) {
+          constexpr int W = N < 32 ? N : 32;
 #pragma unroll
-        for (int r = 0; r < N; r += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(s_neg + r);
-          k8_unpair(k8_fma2(k8_pair(y[r], y[r + 1]), ct2, k8_add2(et2, k8_pair(m.x, m.y))), y[r], y[r + 1]);
-          k8_unpair(k8_fma2(k8_pair(y[r + 2], y[r + 3]), ct2, k8_add2(et2, k8_pair(m.z, m.w))), y[r + 2], y[r + 3]);
+          for (int e = 0; e < W; e += 16) k8_ld16(lane_base + SCOL + c0 + e, y + c0 + e);
+#pragma unroll
+          for (int e = 0; e < W; e += 16) k8_ld_wait16(y + c0 + e);
+#pragma unroll
+          for (int r = c0; r < c0 + W; r += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(s_neg + r);
+            uint64_t y0 = k8_pair(y[r], y[r + 1]), y1 = k8_pair(y[r + 2], y[r + 3]);
+            const float4 f = *reinterpret_cast<const float4*>(s_qf + r);
+            y0 = k8_mul2(y0, k8_pair(f.x, f.y));
+            y1 = k8_mul2(y1, k8_pair(f.z, f.w));
+            k8_unpair(k8_fma2(y0, ct2, k8_add2(et2, k8_pair(m.x, m.y))), y[r], y[r + 1]);
+            k8_unpair(k8_fma2(y1, ct2, k8_add2(et2, k8_pair(m.z, m.w))), y[r + 2], y[r + 3]);
+          }
         }
         if (masked)
 #pragma unroll
@@ -565,12 +621,16 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
             y[r + 2] = pos >= lo.z && pos <= hi.z ? y[r + 2] : -INFINITY;
             y[r + 3] = pos >= lo.w && pos <= hi.w ? y[r + 3] : -INFINITY;
           }
-      };
-      scores();
-      float top = y[0];
+        if (again) break;
+        float t4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-      for (int r = 1; r < N; ++r) top = fmaxf(top, y[r]);
-      if (k8_vote(pending || top > K8_SLACK + K8_BIAS)) {
+        for (int r = 4; r + 8 <= N; r += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t4[e] = k8_max3(t4[e], y[r + 2 * e], y[r + 2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], y[N - 4 + e]);
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        if (!k8_vote(pending || top > K8_SLACK + K8_BIAS)) break;
         // M of some row moves: the chunk's largest term of every row.  A row
         // without a term so far takes it as M, another only if it is past the slack.
 #pragma unroll
@@ -598,44 +658,47 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
 #pragma unroll
         for (int r = 0; r < N; ++r) l[r] *= s_fac[r];
         if (i > 0) {
+          k8_wait(k8_addr(&s_o), (uint32_t)(i - 1) & 1u, ok, g.err);
+          k8_fence_after();
 #pragma unroll
           for (int cc = 0; cc < N; cc += 16) {
             float o[16];
-            k8_ld<16>(lane_base + OCOL + cc, o);
+            k8_ld16(lane_base + OCOL + cc, o);
+            k8_ld_wait16(o);
             uint32_t w[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(o[r] * s_fac[cc + r]);
             k8_st16(lane_base + OCOL + cc, w);
           }
         }
-        scores();
       }
+      k8_fence_before();
+      __syncwarp();
+      if (lane == 0) k8_arrive(k8_addr(&s_r));  // the next chunk's scores may overwrite these
+
+      // ---- terms and their sums
+      uint32_t pk[N / 2];
+#pragma unroll
+      for (int r = 0; r < N; r += 2) {
+        const float p0 = k8_ex2(y[r]), p1 = k8_ex2(y[r + 1]);
+        k8_unpair(k8_fma2(k8_pair(p0, p1), ie2, k8_pair(l[r], l[r + 1])), l[r], l[r + 1]);
+        const __half2 h = __floats2half2_rn(p0, p1);
+        pk[r / 2] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+
+      // ---- P, once the last chunk's product has read its own
+      if (i > 0) k8_wait(k8_addr(&s_o), (uint32_t)(i - 1) & 1u, ok, g.err);
+      k8_fence_after();
       uint8_t* prow = sm + L::P + t * 128;
 #pragma unroll
-      for (int r = 0; r < N; r += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 8; u += 2) {
-          const float p0 = k8_ex2(y[r + u]), p1 = k8_ex2(y[r + u + 1]);
-          k8_unpair(k8_fma2(k8_pair(p0, p1), ie2, k8_pair(l[r + u], l[r + u + 1])), l[r + u], l[r + u + 1]);
-          const __half2 h = __floats2half2_rn(p0, p1);
-          w[u / 2] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(prow + (((r >> 3) ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int r = 0; r < N; r += 8)
+        *reinterpret_cast<uint4*>(prow + (((r >> 3) ^ (t & 7)) << 4)) =
+            make_uint4(pk[r / 2], pk[r / 2 + 1], pk[r / 2 + 2], pk[r / 2 + 3]);
       k8_st_wait();
       k8_fence_smem();
       k8_fence_before();
-      k8_sync();
-      if (t == 0) {
-        k8_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < K8_CHUNK / 16; ++kk)
-          k8_mma(tmem + OCOL, tmem + VCOL + 8 * kk, pd + (uint64_t)((kk * 2048) >> 4), k8_idesc(N, true),
-                 i > 0 || kk > 0);
-        k8_commit(k8_addr(&s_o));
-      }
-      if (i + 1 < n_mine) keys(i + 1);
+      __syncwarp();
+      if (lane == 0) k8_arrive(k8_addr(&s_p));
     }
     if (n_mine > 0) k8_wait(k8_addr(&s_o), (uint32_t)(n_mine - 1) & 1u, ok, g.err);
     k8_fence_after();
@@ -674,20 +737,20 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
       // the whole of every row is here
       if (t < nr) s_fac[t] = s_l[t] == 0.f ? 0.f : 1.f / s_l[t];
       if (t < nr && a.lse)
-        a.lse[(size_t)(sq.row0 + (r0 + t) / G) * a.q_heads + head * G + (r0 + t) % G] =
+        a.lse[(size_t)s_tok[t] * a.q_heads + s_hd[t]] =
             s_l[t] == 0.f ? -INFINITY : (s_m[t] == -INFINITY ? s_l[t] : 0.6931471805599453f * (s_m[t] - K8_BIAS) + logf(s_l[t]));
       k8_sync();
 #pragma unroll 1
       for (int cc = 0; cc < N && cc < nr; cc += 16) {
         float o[16];
-        if (n_mine > 0) k8_ld<16>(lane_base + OCOL + cc, o);
+        k8_ld16(lane_base + OCOL + cc, o);  // anything if no product was made: not used then
+        k8_ld_wait16(o);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int rr = cc + r;
           if (rr >= nr || t >= HD) continue;
           const float v = n_mine > 0 && s_l[rr] != 0.f ? o[r] * s_fac[rr] : 0.f;
-          a.out[(long long)(sq.row0 + (r0 + rr) / G) * a.os + (size_t)(head * G + (r0 + rr) % G) * HD + t] =
-              __float2bfloat16_rn(v);
+          a.out[s_tok[rr] * a.os + s_hd[rr] * HD + t] = __float2bfloat16_rn(v);
         }
       }
     } else if (n_mine > 0) {
@@ -695,7 +758,8 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
 #pragma unroll 1
       for (int cc = 0; cc < N && cc < nr; cc += 16) {
         float o[16];
-        k8_ld<16>(lane_base + OCOL + cc, o);
+        k8_ld16(lane_base + OCOL + cc, o);
+        k8_ld_wait16(o);
         if (t < HD)
 #pragma unroll
           for (int r = 0; r < 16; ++r) part[(cc + r) * L::OLD + t] = o[r];
@@ -706,43 +770,71 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
   }
   k8_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 5) {
     k8_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(K8_COLS) : "memory");
   }
   if (C == 1) return;
 
-  // ---- merge: rank q finishes rows q, q + C, ..., HD / 4 threads to a row
+  // ---- merge: rank q finishes rows q, q + C, ...: first the parts' weights,
+  // then HD / 4 threads to a row
   k8_cluster_sync();
-  constexpr int TPR = HD / 4, RPP = 128 / TPR;
+  __shared__ float s_w[16][N], s_sum[N], s_top[N];
+  const int mine = nr > rank ? (nr - rank + C - 1) / C : 0;
   if (warp < 4) {
-    const uint32_t part = k8_addr(sm), sl = k8_addr(s_l), smx = k8_addr(s_m);
-    const int d = (threadIdx.x % TPR) * 4;
-    for (int r = rank + C * (threadIdx.x / TPR); r < nr; r += C * RPP) {
-      float M = -INFINITY;
-      for (int q = 0; q < C; ++q) M = fmaxf(M, k8_remote_f(k8_remote(smx + r * 4, q)));
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < C; ++q) {
-        const float lq = k8_remote_f(k8_remote(sl + r * 4, q));
-        if (lq == 0.f) continue;  // no key of this row there
-        const float w = k8_ex2(k8_remote_f(k8_remote(smx + r * 4, q)) - M);
-        const float4 x = k8_remote_f4(k8_remote(part + (r * L::OLD + d) * 4, q));
-        sum = fmaf(lq, w, sum);
-        o.x = fmaf(x.x, w, o.x);
-        o.y = fmaf(x.y, w, o.y);
-        o.z = fmaf(x.z, w, o.z);
-        o.w = fmaf(x.w, w, o.w);
+    for (int r = threadIdx.x >> 4; r < mine; r += 8) {  // 16 lanes to a row, one per rank
+      const int row = rank + C * r, q = lane & 15;
+      float m = -INFINITY, lq = 0.f;
+      if (q < C) {
+        m = k8_remote_f(k8_remote(k8_addr(s_m) + row * 4, q));
+        lq = k8_remote_f(k8_remote(k8_addr(s_l) + row * 4, q));
       }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const long long row = sq.row0 + (r0 + r) / G;
-      const int hq = head * G + (r0 + r) % G;
+      const uint32_t half = 0xffffu << (lane & 16);
+      float M = m;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
+      const float w = lq == 0.f ? 0.f : k8_ex2(m - M);  // 0: no key of this row there
+      float sum = lq * w;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
+      s_w[q][r] = w;
+      if (q == 0) {
+        s_sum[r] = sum;
+        s_top[r] = M;
+      }
+    }
+    k8_sync();
+    constexpr int TPR = HD / 4;
+    const int d = (threadIdx.x % TPR) * 4;
+    for (int r = threadIdx.x / TPR; r < mine; r += 128 / TPR) {
+      const int row = rank + C * r;
+      const uint32_t part = k8_addr(sm) + (row * L::OLD + d) * 4;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q0 = 0; q0 < C; q0 += 4) {
+        float4 x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (q0 + e < C && s_w[q0 + e][r] != 0.f) x[e] = k8_remote_f4(k8_remote(part, q0 + e));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = q0 + e < C ? s_w[q0 + e][r] : 0.f;
+          o.x = fmaf(x[e].x, w, o.x);
+          o.y = fmaf(x[e].y, w, o.y);
+          o.z = fmaf(x[e].z, w, o.z);
+          o.w = fmaf(x[e].w, w, o.w);
+        }
+      }
+      const float sum = s_sum[r], M = s_top[r], inv = sum == 0.f ? 0.f : 1.f / sum;
+      const long long at = s_tok[row];
+      const int hq = s_hd[row];
       const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv),
                            b1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(a.out + row * a.os + (size_t)hq * HD + d) =
+      *reinterpret_cast<uint2*>(a.out + at * a.os + (size_t)hq * HD + d) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
       if (d == 0 && a.lse)
-        a.lse[(size_t)row * a.q_heads + hq] =
+        a.lse[(size_t)at * a.q_heads + hq] =
             sum == 0.f ? -INFINITY : (M == -INFINITY ? sum : 0.6931471805599453f * (M - K8_BIAS) + logf(sum));
     }
   }
