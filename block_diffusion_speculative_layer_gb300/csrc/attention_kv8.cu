@@ -1,8 +1,8 @@
 // Attention of a chunk of new tokens over the 8-bit paged cache, on the
 // tensor cores (tcgen05 + TMEM + TMA), sm_103a.
 //
-// A tile is up to N (16, 32 or 64) query rows of one sequence and KV head:
-// row r of the tile is query token r / G, head r % G of the group.  The keys
+// A tile is up to N (16, 32, 64 or 128) query rows of one sequence and KV
+// head: row r of the tile is query token r / G, head r % G of the group.  The keys
 // come in chunks of 128 positions.  Per chunk
 //   S^T [128 keys][N]  = K [128][hd] . (Qhi + Qlo)^T   A = K (e4m3, as cached)
 //   P^T                = 2^(s c_t + e_t - M_r)
@@ -35,12 +35,15 @@
 // The CTAs of a cluster take every C-th chunk of a tile and add their parts
 // through distributed shared memory in rank order.
 //
-// Roles (192 threads): warps 0-3 widen values and run the softmax; warp 4
-// stages keys, values and exponents by TMA in two stages each; warp 5 issues
-// the tensor-core instructions and owns the tensor memory.  S leaves tensor
-// memory for registers at once, so the next chunk's S is computed while the
-// softmax of this one runs.  Two CTAs fit on an SM (256 columns and less than
-// 113 KB each) and fill each other's waits.
+// Roles: GROUPS groups of four warps widen values and run the softmax, each
+// group on its N / GROUPS query rows (a thread's columns of S) and its share
+// of the chunk's values; one warp stages keys, values and exponents by TMA;
+// one issues the tensor-core instructions and owns the tensor memory.  S
+// leaves tensor memory for registers at once, so the next chunk's S is
+// computed while the softmax of this one runs.  Tiles of up to 64 rows run two
+// CTAs to an SM (256 columns, less than 113 KB and 2 groups each), which fill
+// each other's waits; tiles of 128 rows run one (512 columns, 4 groups) and
+// widen a value and read an A operand for twice the rows.
 //
 // Every wait is bounded (about two seconds).  A thread whose wait ran out
 // flags it and goes on without waiting, so all threads reach every barrier.
@@ -64,37 +67,56 @@ struct Kv8Attn {
 };
 
 constexpr int K8_CHUNK = 128;     // keys per chunk: one per tensor-memory lane
-constexpr int K8_STAGES = 2;
-constexpr int K8_THREADS = 192;
 constexpr int K8_SMS = 152;
-constexpr int K8_COLS = 256;      // tensor-memory columns of a CTA
 constexpr float K8_SLACK = 8.f;   // how far (log2) a term may pass M before M moves
 constexpr float K8_BIAS = 6.f;    // P = 2^K8_BIAS for a term at M
 constexpr unsigned long long K8_WAIT_NS = 2000000000ull;
 
-// Shared memory of a CTA (offsets from a 1024-byte boundary).
+// Shapes and shared memory of a CTA (offsets from a 1024-byte boundary).
 template <int HD, int N>
-struct K8Smem {
+struct K8 {
+  static constexpr int GROUPS = N == 128 ? 4 : 2;
+  static constexpr int W = N / GROUPS;                  // query rows (columns of S) of a thread
+  static constexpr int CTHREADS = 128 * GROUPS;         // threads that widen and run the softmax
+  static constexpr int THREADS = CTHREADS + 64;
+  static constexpr int PER_SM = N == 128 ? 1 : 2;       // CTAs on an SM
+  static constexpr int COLS = 512 / PER_SM;             // tensor-memory columns of a CTA:
+  static constexpr int VCOL = 0;                        // widened values of an even and an odd chunk (two to a column),
+  static constexpr int SCOL = 128;                      // S,
+  static constexpr int OCOL = SCOL + N;                 // O
+  static_assert(OCOL + N <= COLS, "tensor-memory columns");
+  static constexpr int STAGES = 2 * (3 - PER_SM);
   static constexpr int TILE = K8_CHUNK * HD;            // one stage of key (or value) codes
-  static constexpr int K = 0;
-  static constexpr int V = K + K8_STAGES * TILE;
-  static constexpr int Q = V + K8_STAGES * TILE;        // [hi, lo][N rows][HD] e4m3, swizzled as the keys
-  static constexpr int P = Q + 2 * N * HD;              // [128 keys][128 B], row r at f16 column r, 128-byte swizzle
-  static constexpr int E = P + K8_CHUNK * 128;          // exponent bytes: [stage][128 keys][k|v]
-  static constexpr int END = E + K8_STAGES * K8_CHUNK * 2;
-  static constexpr int BYTES = END + 1024;
-  // partial results for the merge, over the code stages: [N][HD] floats
-  static constexpr int OLD = HD + 4;
-  static_assert(N * OLD * 4 <= Q, "a tile's partial output fits over the stages");
-  static_assert(2 * (BYTES + 4096) <= 227 * 1024, "two CTAs on an SM");
+  static constexpr int KOFF = 0;
+  static constexpr int VOFF = KOFF + STAGES * TILE;
+  static constexpr int QOFF = VOFF + STAGES * TILE;     // [hi, lo][N rows][HD] e4m3, swizzled as the keys
+  static constexpr int POFF = QOFF + 2 * N * HD;        // [N / 64][128 keys][128 B] f16, row r at column r, 128-byte swizzle
+  static constexpr int EOFF = POFF + (N + 63) / 64 * K8_CHUNK * 128;  // exponent bytes: [stage][128 keys][k|v]
+  static constexpr int BOFF = EOFF + STAGES * K8_CHUNK * 2;             // barriers (offsets from BOFF):
+  static constexpr int FK = 0, FV = FK + 8 * STAGES;    // a stage's keys, values and exponents have landed,
+  static constexpr int EK = FV + 8 * STAGES, EV = EK + 8 * STAGES;      // are read,
+  static constexpr int SS = EV + 8 * STAGES;            // S computed,
+  static constexpr int SR = SS + 8;                     // S read, one arrival per softmax warp,
+  static constexpr int PW = SR + 8;                     // V^T and P written,
+  static constexpr int OU = PW + 8;                     // O updated
+  static constexpr int BYTES = BOFF + 256 + 1024;
+  static constexpr int OLD = HD + 4;                    // the merge's partial output, over the code stages: [N][OLD] floats
+  static_assert(N * OLD * 4 <= QOFF, "a tile's partial output fits over the stages");
+  static_assert(PER_SM * (BYTES + 1024 + 128 * N + 1024) <= 228 * 1024, "CTAs on an SM");
 };
 
 __device__ __forceinline__ uint32_t k8_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void k8_bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
-__device__ __forceinline__ void k8_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+// One arrival for the warp, after what its lanes did before.
+__device__ __forceinline__ void k8_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void k8_arrive_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -110,7 +132,8 @@ __device__ __forceinline__ bool k8_test(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool k8_wait_slow(uint32_t bar, uint32_t parity, int* err) {
+__device__ __noinline__ bool k8_wait_slow(uint32_t bar, uint32_t parity, bool ok, int* err) {
+  if (!ok) return false;
   const unsigned long long t0 = device_ns();
   for (uint32_t it = 1; it < (1u << 30); ++it) {
     if (k8_test(bar, parity)) return true;
@@ -121,24 +144,48 @@ __device__ __noinline__ bool k8_wait_slow(uint32_t bar, uint32_t parity, int* er
 }
 // Bounded wait; once one has run out (`ok` false) the thread waits no more.
 __device__ __forceinline__ void k8_wait(uint32_t bar, uint32_t parity, bool& ok, int* err) {
-  if (ok && !k8_test(bar, parity)) ok = k8_wait_slow(bar, parity, err);
+  if (!k8_test(bar, parity)) ok = k8_wait_slow(bar, parity, ok, err);
 }
-__device__ __forceinline__ void k8_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool k8_vote(bool any) {
+// Barriers of a group of four warps (ids 1..8), and of all that widen (9).
+__device__ __forceinline__ void k8_group_sync(int group) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+}
+template <int THREADS>
+__device__ __forceinline__ void k8_all_sync() {
+  asm volatile("bar.sync 9, %0;" ::"n"(THREADS) : "memory");
+}
+__device__ __forceinline__ bool k8_vote(int group, bool any) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 q, %1, 0;\n\t"
-      "bar.red.or.pred p, 2, 128, q;\n\t"
+      "bar.red.or.pred p, %2, 128, q;\n\t"
       "selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(r)
-      : "r"(any ? 1u : 0u)
+      : "r"(any ? 1u : 0u), "r"(5 + group)
       : "memory");
   return r != 0;
 }
 __device__ __forceinline__ void k8_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void k8_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void k8_fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 k8_lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t k8_lds2(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void k8_sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void k8_sts8(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
+}
 
 // 16 key rows (16 x HD bytes) of slab (page, k, head) into swizzled rows.
 __device__ __forceinline__ void k8_load_keys(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int slab) {
@@ -156,11 +203,12 @@ __device__ __forceinline__ void k8_load_bytes(uint32_t dst, const void* src, uin
 
 // Shared-memory descriptors.  Rows of 128 bytes in the 128-byte swizzle (8-row
 // groups 1024 bytes apart) or of 64 bytes in the 64-byte swizzle (512 bytes
-// apart).  K and Q: K-major.  P: MN-major (rows = keys, query rows along a row).
+// apart).  K and Q: K-major.  P: MN-major (rows = keys, 64 query rows along a row;
+// `block` bytes between such column blocks).
 template <int ROW>
-__device__ __forceinline__ uint64_t k8_desc(uint32_t addr) {
+__device__ __forceinline__ uint64_t k8_desc(uint32_t addr, uint32_t block = 16) {
   static_assert(ROW == 128 || ROW == 64, "row bytes");
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)((8 * ROW) >> 4) << 32) |
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)((8 * ROW) >> 4) << 32) |
          ((uint64_t)1 << 46) | ((uint64_t)(ROW == 128 ? 2 : 4) << 61);
 }
 // Instruction descriptor: A and B f16 (kind::f16) or e4m3 (kind::f8f6f4), fp32 accumulator, 128 x N.
@@ -189,17 +237,33 @@ __device__ __forceinline__ void k8_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 columns of the thread's tensor-memory lane.  The load's registers are
-// valid once k8_ld_wait16 has passed them through.
-__device__ __forceinline__ void k8_ld16(uint32_t addr, float* v) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
-               : "r"(addr));
+// W columns (8, 16 or 32) of the thread's tensor-memory lane.
+template <int W>
+__device__ __forceinline__ void k8_ld(uint32_t addr, float* v) {
+  if constexpr (W == 8)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+        : "r"(addr)
+        : "memory");
+  else if constexpr (W == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
 }
-__device__ __forceinline__ void k8_ld_wait16(float* v) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
-               :
+__device__ __forceinline__ void k8_st8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 __device__ __forceinline__ void k8_st16(uint32_t addr, const uint32_t* v) {
@@ -246,13 +310,6 @@ __device__ __forceinline__ float k8_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Largest value over the warp (numbers win over NaN).
-__device__ __forceinline__ float k8_warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t k8_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -296,21 +353,45 @@ __device__ __forceinline__ void k8_widen16(uint4 w, uint32_t* r) {
   }
 }
 
+// W values per lane, each reduced over the warp in the tree xor 16, 8, 4, 2,
+// 1: as long as a lane holds several, it keeps half of them at each step.  The
+// lane's result is v[0], of value number `base`.
+template <int W, typename Op>
+__device__ __forceinline__ int k8_reduce(float* v, Op op) {
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+#pragma unroll
+  for (int o = 16, n = W; o > 0; o >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = (lane & o) != 0;
+#pragma unroll
+      for (int r = 0; r < W / 2; ++r)
+        if (r < n) {
+          const float send = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
+          v[r] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+      base += up ? n : 0;
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    }
+  }
+  return base;
+}
+
 template <int HD, int N>
-__global__ void __launch_bounds__(K8_THREADS, 2)
+__global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
     kv8_attention_kernel(const __grid_constant__ Kv8Attn a, const __grid_constant__ CUtensorMap kmap) {
-  using L = K8Smem<HD, N>;
-  constexpr int VCOL = 0;                    // tensor-memory columns: widened values (128 keys, two to a
-  constexpr int SCOL = 128;                  // column) of an even and an odd chunk, S,
-  constexpr int OCOL = SCOL + N;             // O
-  static_assert(OCOL + N <= K8_COLS, "tensor-memory columns");
+  using L = K8<HD, N>;
+  constexpr int W = L::W, STAGES = L::STAGES, CT = L::CTHREADS;
   extern __shared__ __align__(128) uint8_t k8_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(k8_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t s_fk[K8_STAGES], s_fv[K8_STAGES], s_ek[K8_STAGES], s_ev[K8_STAGES], s_s, s_r, s_p, s_o;
+  const uint32_t smb = k8_addr(sm), bars = smb + L::BOFF;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_live[K8_STAGES];                        // groups of the chunk that hold positions
-  __shared__ __align__(16) float s_m[N], s_neg[N], s_fac[N], s_qf[N], s_l[N];
-  __shared__ __align__(16) int s_lo[N], s_hi[N], s_tok[N], s_hd[N];  // what a row sees; its token and query head
+  __shared__ int s_live[STAGES];                           // groups of the chunk that hold positions
+  __shared__ __align__(16) float s_m[N], s_neg[N], s_del[N], s_fac[N], s_qf[N], s_l[N];
+  __shared__ __align__(16) int s_lo[N], s_hi[N];           // positions a row sees
+  __shared__ int s_tok[N], s_hd[N];                        // a row's token and query head
   __shared__ float s_red[4][N];
 
   const Kv8Geom& g = a.g;
@@ -318,6 +399,7 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
   const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
   const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
   const int G = a.group;
+  constexpr int PRODUCER = CT / 32, ISSUER = PRODUCER + 1;
 
   // The tile's rows; every CTA of a cluster takes the same way out.
   Kv8Seq sq;
@@ -330,225 +412,234 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
   if (nr <= 0) return;
   const int len = sq.pos0 + sq.n;
 
-  // ---- what each row sees, its query as f16, and the barriers
-  for (int r = threadIdx.x; r < N; r += K8_THREADS) {
-    int lo = 0x7fffffff, hi = -1;
-    if (r < nr) {
-      const int j = (r0 + r) / G, pos = sq.pos0 + j;
-      s_tok[r] = sq.row0 + j;
-      s_hd[r] = head * G + (r0 + r) - j * G;
-      lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-      hi = pos < 0 ? -1 : a.causal ? pos : len - 1;
+  // Positions the rows see: they are in position order, so the first and the
+  // last row bound the tile, and what both see all see.  Chunk c of the
+  // sequence belongs to rank c % C.
+  auto lowest = [&](int pos) { return a.window > 0 ? max(0, pos - a.window + 1) : 0; };
+  auto highest = [&](int pos) { return pos < 0 ? -1 : a.causal ? pos : len - 1; };
+  const int pos_first = sq.pos0 + r0 / G, pos_last = sq.pos0 + (r0 + nr - 1) / G;
+  const int full_lo = lowest(pos_last), full_hi = highest(pos_first), end = highest(pos_last) + 1;
+  const int c_end = (end + K8_CHUNK - 1) / K8_CHUNK;
+  int c_first = min(lowest(pos_first), len) / K8_CHUNK;
+  c_first += (rank - c_first % C + C) % C;
+  const unsigned n_mine = c_end > c_first ? (c_end - c_first + C - 1) / C : 0;
+
+  bool ok = true;
+  // Producer, chunk i: lanes 0-7 bring its groups of 16 keys, lanes 8-15 its
+  // groups of values, lanes 16-23 the exponents.
+  auto produce = [&](unsigned i) {
+    const int st = i % STAGES, gr = lane & 7, pos = (c_first + (int)i * C) * K8_CHUNK + gr * 16;
+    int page = -1;
+    if (lane < 24 && pos < len) {
+      page = g.page_table[(size_t)s * g.pt_stride + pos / g.page_tokens];
+      if (page < 0 || page >= g.n_pages) {
+        page = -1;
+        flag_error(g.err, ERR_BOUNDS);
+      }
     }
-    s_lo[r] = lo;
-    s_hi[r] = hi;
-    s_m[r] = -INFINITY;   // no term yet
-    s_neg[r] = K8_BIAS;
-  }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < K8_STAGES; ++i) {
-      k8_bar_init(k8_addr(&s_fk[i]), 1);
-      k8_bar_init(k8_addr(&s_fv[i]), 1);
-      k8_bar_init(k8_addr(&s_ek[i]), 1);
-      k8_bar_init(k8_addr(&s_ev[i]), 4);
+    const uint32_t live = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
+    const int slot = pos % g.page_tokens;
+    if (i >= STAGES) {
+      k8_wait(bars + L::EK + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
     }
-    k8_bar_init(k8_addr(&s_s), 1);  // S computed
-    k8_bar_init(k8_addr(&s_r), 4);  // S read, one arrival per softmax warp
-    k8_bar_init(k8_addr(&s_p), 4);  // V^T and P written
-    k8_bar_init(k8_addr(&s_o), 1);  // O updated
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
-  }
-  if (warp == 5) {
+    if (lane == 0) k8_arrive_tx(bars + L::FK + st * 8, __popc(live) * 16 * HD);
+    __syncwarp();
+    if (lane < 8 && page >= 0)
+      k8_load_keys(smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, slot,
+                   (page * 2) * g.heads + head);
+    if (i >= STAGES) {
+      k8_wait(bars + L::EV + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+    }
+    if (lane == 0) {
+      s_live[st] = (int)live;
+      k8_arrive_tx(bars + L::FV + st * 8, __popc(live) * (16 * HD + 32));
+    }
+    __syncwarp();
+    if (lane >= 8 && lane < 16 && page >= 0)
+      k8_load_bytes(smb + (L::VOFF + st * L::TILE + gr * 16 * HD),
+                    g.codes + kv8_code_at(g, page, 1, head) + (size_t)slot * HD, 16 * HD, bars + L::FV + st * 8);
+    if (lane >= 16 && page >= 0)
+      k8_load_bytes(smb + (L::EOFF + st * K8_CHUNK * 2 + gr * 32), g.exps + kv8_exp_at(g, page, head, slot), 32,
+                    bars + L::FV + st * 8);
+  };
+
+  // Q: LPR lanes to a row, 8 elements each; the loads start here.
+  constexpr int LPR = HD / 8, RPP = CT / LPR, QPASS = (N + RPP - 1) / RPP;
+  const int sub = threadIdx.x % LPR;
+  uint4 qw[QPASS];
+
+  if (warp == PRODUCER) {
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+      for (int i = 0; i < STAGES; ++i) {
+        k8_bar_init(bars + L::FK + i * 8, 1);
+        k8_bar_init(bars + L::FV + i * 8, 1);
+        k8_bar_init(bars + L::EK + i * 8, 1);
+        k8_bar_init(bars + L::EV + i * 8, CT / 32);
+      }
+      k8_bar_init(bars + L::SS, 1);        // S computed
+      k8_bar_init(bars + L::SR, CT / 32);  // S read, one arrival per softmax warp
+      k8_bar_init(bars + L::PW, CT / 32);  // V^T and P written
+      k8_bar_init(bars + L::OU, 1);        // O updated
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    for (unsigned i = 0; i < STAGES && i < n_mine; ++i) produce(i);
+  } else if (warp == ISSUER) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(k8_addr(&s_tmem)),
-                 "n"(K8_COLS)
+                 "n"(L::COLS)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    k8_fence_before();
+  } else {
+#pragma unroll
+    for (int i = 0; i < QPASS; ++i) {
+      const int r = threadIdx.x / LPR + i * RPP;
+      qw[i] = make_uint4(0, 0, 0, 0);
+      if (r < nr) {
+        const int j = (r0 + r) / G, h = head * G + (r0 + r) - j * G;
+        if (sq.pos0 + j >= 0)
+          qw[i] = *reinterpret_cast<const uint4*>(a.q + (sq.row0 + j) * a.qs + (size_t)h * HD + sub * 8);
+        if (sub == 0) {
+          s_tok[r] = sq.row0 + j;
+          s_hd[r] = h;
+          s_lo[r] = lowest(sq.pos0 + j);
+          s_hi[r] = highest(sq.pos0 + j);
+        }
+      } else if (r < N && sub == 0) {
+        s_lo[r] = 0x7fffffff;
+        s_hi[r] = -1;
+      }
+      if (r < N && sub == 0) {
+        s_m[r] = -INFINITY;  // no term yet
+        s_neg[r] = K8_BIAS;
+      }
+    }
   }
-  k8_fence_before();
   __syncthreads();
   k8_fence_after();
   const uint32_t tmem = s_tmem;
 
-  // Chunks of this CTA: chunk c of the sequence belongs to rank c % C.  The
-  // rows are in position order, so the first and the last bound the tile.
-  const int hi_last = s_hi[nr - 1], lo_first = s_lo[0];
-  const int c_end = hi_last < 0 ? 0 : hi_last / K8_CHUNK + 1;
-  int c_first = min(lo_first, len) / K8_CHUNK;
-  c_first += (rank - c_first % C + C) % C;
-  const int n_mine = c_end > c_first ? (c_end - c_first + C - 1) / C : 0;
-
-  bool ok = true;
-  if (warp == 4) {
-    // ============================================================== producer
-    // lanes 0-7 bring a chunk's groups of 16 keys, lanes 8-15 its groups of values, lanes 16-23 the exponents
-    const int gr = lane & 7;
-    for (int i = 0; i < n_mine; ++i) {
-      const int st = i % K8_STAGES, c = c_first + i * C;
-      const int pos = c * K8_CHUNK + gr * 16;
-      int page = -1;
-      if (lane < 24 && pos < len) {
-        page = g.page_table[(size_t)s * g.pt_stride + pos / g.page_tokens];
-        if (page < 0 || page >= g.n_pages) {
-          page = -1;
-          flag_error(g.err, ERR_BOUNDS);
-        }
-      }
-      const uint32_t live = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
-      if (i >= K8_STAGES) {
-        k8_wait(k8_addr(&s_ek[st]), (uint32_t)(i / K8_STAGES - 1) & 1u, ok, g.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
-      const int slot = pos % g.page_tokens;
-      if (lane == 0) {
-        k8_arrive_tx(k8_addr(&s_fk[st]), __popc(live) * 16 * HD);
-      }
-      __syncwarp();
-      if (lane < 8 && page >= 0)
-        k8_load_keys(k8_addr(sm + L::K + st * L::TILE + gr * 16 * HD), &kmap, k8_addr(&s_fk[st]), slot,
-                     (page * 2) * g.heads + head);
-      if (i >= K8_STAGES) {
-        k8_wait(k8_addr(&s_ev[st]), (uint32_t)(i / K8_STAGES - 1) & 1u, ok, g.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-      }
-      if (lane == 0) {
-        s_live[st] = (int)live;
-        k8_arrive_tx(k8_addr(&s_fv[st]), __popc(live) * (16 * HD + 32));
-      }
-      __syncwarp();
-      if (lane >= 16 && page >= 0)
-        k8_load_bytes(k8_addr(sm + L::E + st * K8_CHUNK * 2 + gr * 32), g.exps + kv8_exp_at(g, page, head, slot), 32,
-                      k8_addr(&s_fv[st]));
-      if (lane >= 8 && lane < 16 && page >= 0)
-        k8_load_bytes(k8_addr(sm + L::V + st * L::TILE + gr * 16 * HD),
-                      g.codes + kv8_code_at(g, page, 1, head) + (size_t)slot * HD, 16 * HD, k8_addr(&s_fv[st]));
-    }
+  if (warp == PRODUCER) {
+    for (unsigned i = STAGES; ok && i < n_mine; ++i) produce(i);
     // The other warps wait for every tile, so no copy is in flight when they
     // are done; if a wait ran out, give the copies issued the same time to land.
     if (!ok)
-      for (int b = 0; b < K8_STAGES; ++b)
+      for (int b = 0; b < STAGES; ++b)
         for (uint32_t p = 0; p < 2; ++p) {
-          (void)(k8_test(k8_addr(&s_fk[b]), p) || k8_wait_slow(k8_addr(&s_fk[b]), p, g.err));
-          (void)(k8_test(k8_addr(&s_fv[b]), p) || k8_wait_slow(k8_addr(&s_fv[b]), p, g.err));
+          (void)(k8_test(bars + L::FK + b * 8, p) || k8_wait_slow(bars + L::FK + b * 8, p, true, g.err));
+          (void)(k8_test(bars + L::FV + b * 8, p) || k8_wait_slow(bars + L::FV + b * 8, p, true, g.err));
         }
     __syncwarp();
-  } else if (warp == 5) {
-    // ================================================================ issuer
-    asm volatile("bar.sync 3, 160;" ::: "memory");  // Q is in shared memory
+  } else if (warp == ISSUER) {
+    asm volatile("bar.sync 10, %0;" ::"n"(CT + 32) : "memory");  // Q is in shared memory
     if (lane == 0 && n_mine > 0) {
-      const uint64_t kd = k8_desc<HD>(k8_addr(sm + L::K)), qd = k8_desc<HD>(k8_addr(sm + L::Q)),
-                     pd = k8_desc<128>(k8_addr(sm + L::P));
+      const uint64_t kd = k8_desc<HD>(smb + (L::KOFF)), qd = k8_desc<HD>(smb + (L::QOFF)),
+                     pd = k8_desc<128>(smb + (L::POFF), K8_CHUNK * 128);
       // S^T of chunk i; its key tile is free when that is done
-      auto scores = [&](int i) {
-        const int st = i % K8_STAGES;
-        k8_wait(k8_addr(&s_fk[st]), (uint32_t)(i / K8_STAGES) & 1u, ok, g.err);
+      auto scores = [&](unsigned i) {
+        const int st = i % STAGES;
+        k8_wait(bars + L::FK + st * 8, (i / STAGES) & 1u, ok, g.err);
         k8_fence_after();
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)  // the queries' high halves, then the low ones
-          k8_mma_codes(tmem + SCOL, kd + (uint64_t)((st * L::TILE + kk % (HD / 32) * 32) >> 4),
+          k8_mma_codes(tmem + L::SCOL, kd + (uint64_t)((st * L::TILE + kk % (HD / 32) * 32) >> 4),
                        qd + (uint64_t)((kk / (HD / 32) * N * HD + kk % (HD / 32) * 32) >> 4), k8_idesc(N, false),
                        kk > 0);
-        k8_commit(k8_addr(&s_s));
-        k8_commit(k8_addr(&s_ek[st]));
+        k8_commit(bars + L::SS);
+        k8_commit(bars + L::EK + st * 8);
       };
       scores(0);
-      for (int i = 0; i < n_mine; ++i) {
+      for (unsigned i = 0; i < n_mine; ++i) {
         if (i + 1 < n_mine) {
-          k8_wait(k8_addr(&s_r), (uint32_t)i & 1u, ok, g.err);
+          k8_wait(bars + L::SR, i & 1u, ok, g.err);
           scores(i + 1);
         }
-        k8_wait(k8_addr(&s_p), (uint32_t)i & 1u, ok, g.err);
+        k8_wait(bars + L::PW, i & 1u, ok, g.err);
         k8_fence_after();
 #pragma unroll
         for (int kk = 0; kk < K8_CHUNK / 16; ++kk)
-          k8_mma(tmem + OCOL, tmem + VCOL + (i & 1) * 64 + 8 * kk, pd + (uint64_t)((kk * 2048) >> 4), k8_idesc(N, true),
-                 i > 0 || kk > 0);
-        k8_commit(k8_addr(&s_o));
+          k8_mma(tmem + L::OCOL, tmem + L::VCOL + (i & 1) * 64 + 8 * kk, pd + (uint64_t)((kk * 2048) >> 4),
+                 k8_idesc(N, true), i > 0 || kk > 0);
+        k8_commit(bars + L::OU);
       }
       // every product has finished before tensor memory is freed
       bool done = true;
-      k8_wait(k8_addr(&s_o), (uint32_t)(n_mine - 1) & 1u, done, g.err);
+      k8_wait(bars + L::OU, (n_mine - 1) & 1u, done, g.err);
     }
     __syncwarp();
   } else {
-    // ==================================================== widening, softmax
-    const int t = threadIdx.x;  // tensor-memory lane: the chunk's key t, and head dim t
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const int t = threadIdx.x & 127, group = threadIdx.x >> 7;  // t: tensor-memory lane = the chunk's key, and head dim
+    const int w0 = group * W;                                   // the thread's first column
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 
     // Q as two e4m3 numbers
-    constexpr int LPR = HD / 8, RPP = 128 / LPR, QPASS = (N + RPP - 1) / RPP;  // lanes per row, rows per pass
-    const int sub = t % LPR;
-    {
-      uint4 qw[QPASS];
 #pragma unroll
-      for (int i = 0; i < QPASS; ++i) {  // all loads first
-        const int r = t / LPR + i * RPP;
-        qw[i] = make_uint4(0, 0, 0, 0);
-        if (r < nr && s_hi[r] >= 0)
-          qw[i] = *reinterpret_cast<const uint4*>(a.q + s_tok[r] * a.qs + s_hd[r] * HD + sub * 8);
+    for (int i = 0; i < QPASS; ++i) {
+      const int r = threadIdx.x / LPR + i * RPP;
+      const uint32_t ws[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) top = max(top, max(ws[u] & 0x7FFFu, (ws[u] >> 16) & 0x7FFFu));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // the power of two taken out of the row (a row that holds no numbers becomes NaN)
+      const int out = min(max((int)(top >> 7) - 127 - 7, -119), 120);
+      const float by = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : kv8_pow2(-out);
+      float x[8], hi[8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        x[2 * u] = __uint_as_float(ws[u] << 16) * by;
+        x[2 * u + 1] = __uint_as_float(ws[u] & 0xFFFF0000u) * by;
+      }
+      const uint2 ch = make_uint2(kv8_pack4(x[0], x[1], x[2], x[3]), kv8_pack4(x[4], x[5], x[6], x[7]));
+      const uint32_t two[4] = {ch.x & 0xFFFFu, ch.x >> 16, ch.y & 0xFFFFu, ch.y >> 16};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 f = kv8_value2(two[u]);
+        hi[2 * u] = f.x;
+        hi[2 * u + 1] = f.y;
       }
 #pragma unroll
-      for (int i = 0; i < QPASS; ++i) {
-        const int r = t / LPR + i * RPP;
-        const uint32_t ws[4] = {qw[i].x, qw[i].y, qw[i].z, qw[i].w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) top = max(top, max(ws[u] & 0x7FFFu, (ws[u] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // the power of two taken out of the row (a row that holds no numbers becomes NaN)
-        const int out = min(max((int)(top >> 7) - 127 - 7, -119), 120);
-        const float by = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : kv8_pow2(-out);
-        float x[8], hi[8];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          x[2 * u] = __uint_as_float(ws[u] << 16) * by;
-          x[2 * u + 1] = __uint_as_float(ws[u] & 0xFFFF0000u) * by;
-        }
-        const uint2 ch = make_uint2(kv8_pack4(x[0], x[1], x[2], x[3]), kv8_pack4(x[4], x[5], x[6], x[7]));
-        const uint32_t two[4] = {ch.x & 0xFFFFu, ch.x >> 16, ch.y & 0xFFFFu, ch.y >> 16};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float2 f = kv8_value2(two[u]);
-          hi[2 * u] = f.x;
-          hi[2 * u + 1] = f.y;
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] -= hi[u];
-        const uint2 cl = make_uint2(kv8_pack4(x[0], x[1], x[2], x[3]), kv8_pack4(x[4], x[5], x[6], x[7]));
-        if (r < N) {
-          const int piece = sub >> 1, at = HD == 128 ? (piece ^ (r & 7)) : (piece ^ ((r >> 1) & 3));
-          uint8_t* dst = sm + L::Q + r * HD + at * 16 + (sub & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = ch;
-          *reinterpret_cast<uint2*>(dst + N * HD) = cl;
-          if (sub == 0) s_qf[r] = kv8_pow2(out);
-        }
+      for (int u = 0; u < 8; ++u) x[u] -= hi[u];
+      const uint2 cl = make_uint2(kv8_pack4(x[0], x[1], x[2], x[3]), kv8_pack4(x[4], x[5], x[6], x[7]));
+      if (r < N) {
+        const int piece = sub >> 1, at = HD == 128 ? (piece ^ (r & 7)) : (piece ^ ((r >> 1) & 3));
+        const uint32_t dst = smb + L::QOFF + r * HD + at * 16 + (sub & 1) * 8;
+        k8_sts8(dst, ch);
+        k8_sts8(dst + N * HD, cl);
+        if (sub == 0) s_qf[r] = kv8_pow2(out);
       }
     }
     k8_fence_smem();
-    asm volatile("bar.arrive 3, 160;" ::: "memory");
-    k8_sync();
+    asm volatile("bar.arrive 10, %0;" ::"n"(CT + 32) : "memory");
+    k8_all_sync<CT>();  // s_qf
 
-    // rows that exist: positions every one of them sees
-    const int full_lo = s_lo[nr - 1], full_hi = s_hi[0];
-    float l[N];
+    float l[W];
 #pragma unroll
-    for (int r = 0; r < N; ++r) l[r] = 0.f;
+    for (int r = 0; r < W; ++r) l[r] = 0.f;
+    constexpr int VSHARE = 8 / L::GROUPS;  // groups of 16 values this thread widens
+    const int v0 = group * VSHARE;
     if (HD < 128 && t >= HD) {  // lanes past the head dims add zeros to rows of O nobody reads
-      const uint32_t z[16] = {};
+      const uint32_t z[8] = {};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) k8_st16(lane_base + VCOL + 16 * i, z);
+      for (int i = 0; i < 2 * VSHARE; ++i)
+        k8_st8(lane_base + L::VCOL + (i / VSHARE) * 64 + (v0 + i % VSHARE) * 8, z);
     }
     bool pending = true;  // some row has no term yet
+    // this key's 16-byte piece of P for column w0 (w0 is a multiple of W, so piece p of the thread is at prow ^ 16 p)
+    const uint32_t prow = smb + L::POFF + (w0 >> 6) * K8_CHUNK * 128 + t * 128 + ((((w0 & 63) >> 3) ^ (t & 7)) << 4);
 
-    for (int i = 0; i < n_mine; ++i) {
-      const int st = i % K8_STAGES, key0 = (c_first + i * C) * K8_CHUNK;
+    for (unsigned i = 0; i < n_mine; ++i) {
+      const int st = i % STAGES, key0 = (c_first + (int)i * C) * K8_CHUNK;
       // ---- this key's scales
-      k8_wait(k8_addr(&s_fv[st]), (uint32_t)(i / K8_STAGES) & 1u, ok, g.err);
+      k8_wait(bars + L::FV + st * 8, (i / STAGES) & 1u, ok, g.err);
       const int live = s_live[st];
-      const uint32_t ee = *reinterpret_cast<const uint16_t*>(sm + L::E + st * K8_CHUNK * 2 + t * 2);
+      const uint32_t ee = k8_lds2(smb + L::EOFF + st * K8_CHUNK * 2 + t * 2);
       const bool here = (live >> (t >> 4)) & 1;
       const int bk = ee & 255, bv = ee >> 8;
       const float ct = here ? kv8_scale(bk) * a.scale_log2 : 0.f;
@@ -560,126 +651,120 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
 
       // ---- values (the product of two chunks ago has read this buffer: O's wait below)
       if (HD == 128 || t < HD) {
-        const uint8_t* row = sm + L::V + st * L::TILE + t * 16;
-        const bool tail = live != 0xff || key0 + K8_CHUNK > len;
+        const uint32_t row = smb + L::VOFF + st * L::TILE + v0 * 16 * HD + t * 16;
+        uint4 v[VSHARE];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 v[4];
+        for (int q = 0; q < VSHARE; ++q) v[q] = k8_lds16(row + q * 16 * HD);
+        if (live != 0xff || key0 + K8_CHUNK > len) {  // bytes behind the last position may be anything: zeros
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = *reinterpret_cast<const uint4*>(row + (4 * h + q) * 16 * HD);
-          if (tail) {  // bytes behind the last position may be anything: zeros
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int gr = 4 * h + q, n = (live >> gr) & 1 ? len - key0 - gr * 16 : 0;
-              v[q].x = n >= 4 ? v[q].x : n <= 0 ? 0u : v[q].x & ((1u << (8 * n)) - 1);
-              v[q].y = n >= 8 ? v[q].y : n <= 4 ? 0u : v[q].y & ((1u << (8 * (n - 4))) - 1);
-              v[q].z = n >= 12 ? v[q].z : n <= 8 ? 0u : v[q].z & ((1u << (8 * (n - 8))) - 1);
-              v[q].w = n >= 16 ? v[q].w : n <= 12 ? 0u : v[q].w & ((1u << (8 * (n - 12))) - 1);
-            }
+          for (int q = 0; q < VSHARE; ++q) {
+            const int gr = v0 + q, n = (live >> gr) & 1 ? len - key0 - gr * 16 : 0;
+            v[q].x = n >= 4 ? v[q].x : n <= 0 ? 0u : v[q].x & ((1u << (8 * n)) - 1);
+            v[q].y = n >= 8 ? v[q].y : n <= 4 ? 0u : v[q].y & ((1u << (8 * (n - 4))) - 1);
+            v[q].z = n >= 12 ? v[q].z : n <= 8 ? 0u : v[q].z & ((1u << (8 * (n - 8))) - 1);
+            v[q].w = n >= 16 ? v[q].w : n <= 12 ? 0u : v[q].w & ((1u << (8 * (n - 12))) - 1);
           }
+        }
 #pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            uint32_t w[16];
-            k8_widen16(v[q], w);
-            k8_widen16(v[q + 1], w + 8);
-            k8_st16(lane_base + VCOL + (i & 1) * 64 + 32 * h + 8 * q, w);
-          }
+        for (int q = 0; q < VSHARE; q += 2) {
+          uint32_t w[16];
+          k8_widen16(v[q], w);
+          k8_widen16(v[q + 1], w + 8);
+          k8_st16(lane_base + L::VCOL + (i & 1) * 64 + (v0 + q) * 8, w);
         }
       }
-      __syncwarp();
-      if (lane == 0) k8_arrive(k8_addr(&s_ev[st]));
+      k8_arrive_warp(bars + L::EV + st * 8);
 
       // ---- its terms' exponents, straight from tensor memory
-      k8_wait(k8_addr(&s_s), (uint32_t)i & 1u, ok, g.err);
+      k8_wait(bars + L::SS, i & 1u, ok, g.err);
       k8_fence_after();
-      float y[N];
-      for (bool again = false;; again = true) {
+      float y[W];
+      k8_ld<W>(lane_base + L::SCOL + w0, y);
+      k8_fence_before();
+      k8_arrive_warp(bars + L::SR);  // the next chunk's scores may overwrite these
 #pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 32) {
-          constexpr int W = N < 32 ? N : 32;
+      for (int r = 0; r < W; r += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(s_neg + w0 + r);
+        const float4 f = *reinterpret_cast<const float4*>(s_qf + w0 + r);
+        const uint64_t y0 = k8_mul2(k8_pair(y[r], y[r + 1]), k8_pair(f.x, f.y)),
+                       y1 = k8_mul2(k8_pair(y[r + 2], y[r + 3]), k8_pair(f.z, f.w));
+        k8_unpair(k8_fma2(y0, ct2, k8_add2(et2, k8_pair(m.x, m.y))), y[r], y[r + 1]);
+        k8_unpair(k8_fma2(y1, ct2, k8_add2(et2, k8_pair(m.z, m.w))), y[r + 2], y[r + 3]);
+      }
+      if (masked)
 #pragma unroll
-          for (int e = 0; e < W; e += 16) k8_ld16(lane_base + SCOL + c0 + e, y + c0 + e);
-#pragma unroll
-          for (int e = 0; e < W; e += 16) k8_ld_wait16(y + c0 + e);
-#pragma unroll
-          for (int r = c0; r < c0 + W; r += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(s_neg + r);
-            uint64_t y0 = k8_pair(y[r], y[r + 1]), y1 = k8_pair(y[r + 2], y[r + 3]);
-            const float4 f = *reinterpret_cast<const float4*>(s_qf + r);
-            y0 = k8_mul2(y0, k8_pair(f.x, f.y));
-            y1 = k8_mul2(y1, k8_pair(f.z, f.w));
-            k8_unpair(k8_fma2(y0, ct2, k8_add2(et2, k8_pair(m.x, m.y))), y[r], y[r + 1]);
-            k8_unpair(k8_fma2(y1, ct2, k8_add2(et2, k8_pair(m.z, m.w))), y[r + 2], y[r + 3]);
-          }
+        for (int r = 0; r < W; r += 4) {
+          const int4 lo = *reinterpret_cast<const int4*>(s_lo + w0 + r);
+          const int4 hi = *reinterpret_cast<const int4*>(s_hi + w0 + r);
+          y[r] = pos >= lo.x && pos <= hi.x ? y[r] : -INFINITY;
+          y[r + 1] = pos >= lo.y && pos <= hi.y ? y[r + 1] : -INFINITY;
+          y[r + 2] = pos >= lo.z && pos <= hi.z ? y[r + 2] : -INFINITY;
+          y[r + 3] = pos >= lo.w && pos <= hi.w ? y[r + 3] : -INFINITY;
         }
-        if (masked)
+      float t4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-          for (int r = 0; r < N; r += 4) {
-            const int4 lo = *reinterpret_cast<const int4*>(s_lo + r), hi = *reinterpret_cast<const int4*>(s_hi + r);
-            y[r] = pos >= lo.x && pos <= hi.x ? y[r] : -INFINITY;
-            y[r + 1] = pos >= lo.y && pos <= hi.y ? y[r + 1] : -INFINITY;
-            y[r + 2] = pos >= lo.z && pos <= hi.z ? y[r + 2] : -INFINITY;
-            y[r + 3] = pos >= lo.w && pos <= hi.w ? y[r + 3] : -INFINITY;
-          }
-        if (again) break;
-        float t4[4] = {y[0], y[1], y[2], y[3]};
+      for (int r = 4; r + 8 <= W; r += 8)
 #pragma unroll
-        for (int r = 4; r + 8 <= N; r += 8)
+        for (int e = 0; e < 4; ++e) t4[e] = k8_max3(t4[e], y[r + 2 * e], y[r + 2 * e + 1]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t4[e] = k8_max3(t4[e], y[r + 2 * e], y[r + 2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], y[N - 4 + e]);
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        if (!k8_vote(pending || top > K8_SLACK + K8_BIAS)) break;
+      for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], y[W - 4 + e]);
+      const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      if (k8_vote(group, pending || top > K8_SLACK + K8_BIAS)) {
         // M of some row moves: the chunk's largest term of every row.  A row
         // without a term so far takes it as M, another only if it is past the slack.
+        {
+          float v[W];
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-          const float w = k8_warp_max(y[r]);
-          if (lane == (r & 31)) s_red[warp][r] = w;
+          for (int r = 0; r < W; ++r) v[r] = y[r];
+          const int base = k8_reduce<W>(v, [](float p, float q) { return fmaxf(p, q); });
+          s_red[warp & 3][w0 + base] = v[0];
         }
-        k8_sync();
+        k8_group_sync(group);
         bool wait = false;
-        if (t < N) {
-          const float ym = fmaxf(fmaxf(s_red[0][t], s_red[1][t]), fmaxf(s_red[2][t], s_red[3][t]));
-          float fac = 1.f, m = s_m[t];
+        if (t < W) {
+          const int r = w0 + t;
+          const float ym = fmaxf(fmaxf(s_red[0][r], s_red[1][r]), fmaxf(s_red[2][r], s_red[3][r]));
+          float fac = 1.f, m = s_m[r];
           if (m == -INFINITY) {
             if (ym > -INFINITY) m = ym - K8_BIAS;
           } else if (ym > K8_SLACK + K8_BIAS) {
             m += ym - K8_BIAS;
-            fac = k8_ex2(s_m[t] - m);
+            fac = k8_ex2(s_m[r] - m);
           }
-          if (m > -INFINITY) s_neg[t] = K8_BIAS - m;
-          s_m[t] = m;
-          s_fac[t] = fac;
-          wait = t < nr && s_hi[t] >= 0 && m == -INFINITY;
+          const float neg = m > -INFINITY ? K8_BIAS - m : K8_BIAS;
+          s_del[r] = neg - s_neg[r];
+          s_neg[r] = neg;
+          s_m[r] = m;
+          s_fac[r] = fac;
+          wait = r < nr && s_hi[r] >= 0 && m == -INFINITY;
         }
-        pending = k8_vote(wait);
+        pending = k8_vote(group, wait);
 #pragma unroll
-        for (int r = 0; r < N; ++r) l[r] *= s_fac[r];
+        for (int r = 0; r < W; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s_fac + w0 + r);
+          const float4 d = *reinterpret_cast<const float4*>(s_del + w0 + r);
+          l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
+          y[r] += d.x, y[r + 1] += d.y, y[r + 2] += d.z, y[r + 3] += d.w;
+        }
         if (i > 0) {
-          k8_wait(k8_addr(&s_o), (uint32_t)(i - 1) & 1u, ok, g.err);
+          k8_wait(bars + L::OU, (i - 1) & 1u, ok, g.err);
           k8_fence_after();
 #pragma unroll
-          for (int cc = 0; cc < N; cc += 16) {
-            float o[16];
-            k8_ld16(lane_base + OCOL + cc, o);
-            k8_ld_wait16(o);
-            uint32_t w[16];
+          for (int cc = 0; cc < W; cc += 8) {
+            float o[8];
+            k8_ld<8>(lane_base + L::OCOL + w0 + cc, o);
+            uint32_t w[8];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) w[r] = __float_as_uint(o[r] * s_fac[cc + r]);
-            k8_st16(lane_base + OCOL + cc, w);
+            for (int r = 0; r < 8; ++r) w[r] = __float_as_uint(o[r] * s_fac[w0 + cc + r]);
+            k8_st8(lane_base + L::OCOL + w0 + cc, w);
           }
         }
       }
-      k8_fence_before();
-      __syncwarp();
-      if (lane == 0) k8_arrive(k8_addr(&s_r));  // the next chunk's scores may overwrite these
 
       // ---- terms and their sums
-      uint32_t pk[N / 2];
+      uint32_t pk[W / 2];
 #pragma unroll
-      for (int r = 0; r < N; r += 2) {
+      for (int r = 0; r < W; r += 2) {
         const float p0 = k8_ex2(y[r]), p1 = k8_ex2(y[r + 1]);
         k8_unpair(k8_fma2(k8_pair(p0, p1), ie2, k8_pair(l[r], l[r + 1])), l[r], l[r + 1]);
         const __half2 h = __floats2half2_rn(p0, p1);
@@ -687,102 +772,75 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
       }
 
       // ---- P, once the last chunk's product has read its own
-      if (i > 0) k8_wait(k8_addr(&s_o), (uint32_t)(i - 1) & 1u, ok, g.err);
+      if (i > 0) k8_wait(bars + L::OU, (i - 1) & 1u, ok, g.err);
       k8_fence_after();
-      uint8_t* prow = sm + L::P + t * 128;
 #pragma unroll
-      for (int r = 0; r < N; r += 8)
-        *reinterpret_cast<uint4*>(prow + (((r >> 3) ^ (t & 7)) << 4)) =
-            make_uint4(pk[r / 2], pk[r / 2 + 1], pk[r / 2 + 2], pk[r / 2 + 3]);
+      for (int r = 0; r < W; r += 8)
+        k8_sts16(prow ^ (r * 2), pk[r / 2], pk[r / 2 + 1], pk[r / 2 + 2], pk[r / 2 + 3]);
       k8_st_wait();
       k8_fence_smem();
       k8_fence_before();
-      __syncwarp();
-      if (lane == 0) k8_arrive(k8_addr(&s_p));
+      k8_arrive_warp(bars + L::PW);
     }
-    if (n_mine > 0) k8_wait(k8_addr(&s_o), (uint32_t)(n_mine - 1) & 1u, ok, g.err);
+    if (n_mine > 0) k8_wait(bars + L::OU, (n_mine - 1) & 1u, ok, g.err);
     k8_fence_after();
 
-    // ---- sums over the keys: halve the rows a lane carries, the same tree for every row
-    {
-      float v[N];
-#pragma unroll
-      for (int r = 0; r < N; ++r) v[r] = l[r];
-      int base = 0;
-#pragma unroll
-      for (int o = 16, n = N; o > 0; o >>= 1) {
-        if (n > 1) {
-          n >>= 1;
-          const bool up = (lane & o) != 0;
-#pragma unroll
-          for (int r = 0; r < N / 2; ++r)
-            if (r < n) {
-              const float send = up ? v[r] : v[r + n], keep = up ? v[r + n] : v[r];
-              v[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-            }
-          base += up ? n : 0;
-        } else {
-          v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-        }
-      }
-      constexpr int LEFT = N > 32 ? N / 32 : 1;
-#pragma unroll
-      for (int r = 0; r < LEFT; ++r) s_red[warp][base + r] = v[r];
-    }
-    k8_sync();
-    if (t < N) s_l[t] = ((s_red[0][t] + s_red[1][t]) + s_red[2][t]) + s_red[3][t];
-    k8_sync();
+    // ---- sums over the keys
+    const int base = k8_reduce<W>(l, [](float p, float q) { return p + q; });
+    s_red[warp & 3][w0 + base] = l[0];
+    k8_group_sync(group);
+    if (t < W) s_l[w0 + t] = ((s_red[0][w0 + t] + s_red[1][w0 + t]) + s_red[2][w0 + t]) + s_red[3][w0 + t];
+    k8_group_sync(group);
 
     if (C == 1) {
       // the whole of every row is here
-      if (t < nr) s_fac[t] = s_l[t] == 0.f ? 0.f : 1.f / s_l[t];
-      if (t < nr && a.lse)
-        a.lse[(size_t)s_tok[t] * a.q_heads + s_hd[t]] =
-            s_l[t] == 0.f ? -INFINITY : (s_m[t] == -INFINITY ? s_l[t] : 0.6931471805599453f * (s_m[t] - K8_BIAS) + logf(s_l[t]));
-      k8_sync();
+      if (t < W && w0 + t < nr) {
+        const int r = w0 + t;
+        const float sum = s_l[r];
+        s_fac[r] = sum == 0.f ? 0.f : 1.f / sum;
+        if (a.lse)
+          a.lse[(size_t)s_tok[r] * a.q_heads + s_hd[r]] =
+              sum == 0.f ? -INFINITY : (s_m[r] == -INFINITY ? sum : 0.6931471805599453f * (s_m[r] - K8_BIAS) + logf(sum));
+      }
+      k8_group_sync(group);
 #pragma unroll 1
-      for (int cc = 0; cc < N && cc < nr; cc += 16) {
-        float o[16];
-        k8_ld16(lane_base + OCOL + cc, o);  // anything if no product was made: not used then
-        k8_ld_wait16(o);
+      for (int cc = w0; cc < w0 + W && cc < nr; cc += 8) {
+        float o[8];
+        k8_ld<8>(lane_base + L::OCOL + cc, o);  // anything if no product was made: not used then
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int rr = cc + r;
-          if (rr >= nr || t >= HD) continue;
-          const float v = n_mine > 0 && s_l[rr] != 0.f ? o[r] * s_fac[rr] : 0.f;
-          a.out[s_tok[rr] * a.os + s_hd[rr] * HD + t] = __float2bfloat16_rn(v);
+        for (int r = 0; r < 8; ++r) {
+          if (cc + r >= nr || t >= HD) continue;
+          const float v = s_l[cc + r] == 0.f ? 0.f : o[r] * s_fac[cc + r];
+          a.out[s_tok[cc + r] * a.os + s_hd[cc + r] * HD + t] = __float2bfloat16_rn(v);
         }
       }
     } else if (n_mine > 0) {
       float* part = reinterpret_cast<float*>(sm);
 #pragma unroll 1
-      for (int cc = 0; cc < N && cc < nr; cc += 16) {
-        float o[16];
-        k8_ld16(lane_base + OCOL + cc, o);
-        k8_ld_wait16(o);
+      for (int cc = w0; cc < w0 + W && cc < nr; cc += 8) {
+        float o[8];
+        k8_ld<8>(lane_base + L::OCOL + cc, o);
         if (t < HD)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) part[(cc + r) * L::OLD + t] = o[r];
+          for (int r = 0; r < 8; ++r) part[(cc + r) * L::OLD + t] = o[r];
       }
-    } else {
-      if (t < N) s_l[t] = 0.f;
     }
   }
   k8_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == ISSUER) {
     k8_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(K8_COLS) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::COLS) : "memory");
   }
   if (C == 1) return;
 
   // ---- merge: rank q finishes rows q, q + C, ...: first the parts' weights,
   // then HD / 4 threads to a row
   k8_cluster_sync();
-  __shared__ float s_w[16][N], s_sum[N], s_top[N];
+  __shared__ float s_w[16][(N + 1) / 2], s_sum[(N + 1) / 2], s_top[(N + 1) / 2];
   const int mine = nr > rank ? (nr - rank + C - 1) / C : 0;
-  if (warp < 4) {
-    for (int r = threadIdx.x >> 4; r < mine; r += 8) {  // 16 lanes to a row, one per rank
+  if (warp < PRODUCER) {
+    for (int r = threadIdx.x >> 4; r < mine; r += CT / 16) {  // 16 lanes to a row, one per rank
       const int row = rank + C * r, q = lane & 15;
       float m = -INFINITY, lq = 0.f;
       if (q < C) {
@@ -803,12 +861,12 @@ __global__ void __launch_bounds__(K8_THREADS, 2)
         s_top[r] = M;
       }
     }
-    k8_sync();
+    k8_all_sync<CT>();
     constexpr int TPR = HD / 4;
     const int d = (threadIdx.x % TPR) * 4;
-    for (int r = threadIdx.x / TPR; r < mine; r += 128 / TPR) {
+    for (int r = threadIdx.x / TPR; r < mine; r += CT / TPR) {
       const int row = rank + C * r;
-      const uint32_t part = k8_addr(sm) + (row * L::OLD + d) * 4;
+      const uint32_t part = smb + (row * L::OLD + d) * 4;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int q0 = 0; q0 < C; q0 += 4) {
         float4 x[4];
@@ -869,7 +927,7 @@ static bool k8_tmap(CUtensorMap* map, const Kv8Geom& g) {
 template <int HD, int N>
 static cudaError_t k8_attrs() {
   cudaError_t e = cudaFuncSetAttribute(kv8_attention_kernel<HD, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       K8Smem<HD, N>::BYTES);
+                                       K8<HD, N>::BYTES);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(kv8_attention_kernel<HD, N>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   return e;
@@ -887,8 +945,8 @@ static cudaError_t k8_launch(const Kv8Attn& a, const CUtensorMap& map, int clust
   }
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)((long long)cluster * a.g.nseq * a.tiles), a.g.heads, 1);
-  c.blockDim = dim3(K8_THREADS);
-  c.dynamicSmemBytes = K8Smem<HD, N>::BYTES;
+  c.blockDim = dim3(K8<HD, N>::THREADS);
+  c.dynamicSmemBytes = K8<HD, N>::BYTES;
   c.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -941,7 +999,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   // the narrowest tile that holds a sequence's rows, or the widest
   const long long wanted = (long long)a.max_rows * a.group;
-  const int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : 64;
+  const int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : wanted <= 64 ? 64 : 128;
   const long long tiles = (wanted + n - 1) / n;
   if (tiles * nseq > 0x7fffffff / 16) return DF_EINVAL;
   a.tiles = (int)tiles;
@@ -957,11 +1015,15 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (head_dim == 128)
-    e = n == 16 ? k8_launch<128, 16>(a, map, cluster, st)
-                : n == 32 ? k8_launch<128, 32>(a, map, cluster, st) : k8_launch<128, 64>(a, map, cluster, st);
+    e = n == 16   ? k8_launch<128, 16>(a, map, cluster, st)
+        : n == 32 ? k8_launch<128, 32>(a, map, cluster, st)
+        : n == 64 ? k8_launch<128, 64>(a, map, cluster, st)
+                  : k8_launch<128, 128>(a, map, cluster, st);
   else
-    e = n == 16 ? k8_launch<64, 16>(a, map, cluster, st)
-                : n == 32 ? k8_launch<64, 32>(a, map, cluster, st) : k8_launch<64, 64>(a, map, cluster, st);
+    e = n == 16   ? k8_launch<64, 16>(a, map, cluster, st)
+        : n == 32 ? k8_launch<64, 32>(a, map, cluster, st)
+        : n == 64 ? k8_launch<64, 64>(a, map, cluster, st)
+                  : k8_launch<64, 128>(a, map, cluster, st);
   return e == cudaSuccess ? DF_OK : DF_ECUDA;
 }
 
