@@ -608,51 +608,64 @@ def kv8_check(cache: KV8Cache):
 
 
 _I32_MAX = 2 ** 31 - 1
+_kv8_env = None  # what the calls below look up once: their time is part of a small step's latency
+
+
+def _kv8_bind():
+    """(uint8, int32, bf16, fp32, raw current stream of a device, current device, the three entry points)."""
+    global _kv8_env
+    if _kv8_env is None:
+        import torch
+        torch.cuda.init()
+        L = lib()
+        _kv8_env = (torch.uint8, torch.int32, torch.bfloat16, torch.float32, torch._C._cuda_getCurrentRawStream,
+                    torch._C._cuda_getDevice, L.df_op_kv8_write, L.df_op_kv8_read, L.df_op_attention_kv8)
+    return _kv8_env
 
 
 def _kv8_refuse(why: str):
     raise DfError(DF_EINVAL, "kv8: " + why)
 
 
-def _kv8_plan(cache: KV8Cache, page_table, row_start, kv_len):
-    """Check the arguments every call shares; (device index, geometry)."""
-    import torch
+def _kv8_plan(cache: KV8Cache, page_table, row_start, kv_len, u8, i32):
+    """Check the arguments every call shares; (device index, codes' shape, sequences, table entries)."""
     codes, exps, err = cache
     dev = codes.get_device()
-    if dev < 0:
-        _kv8_refuse("the cache must be on a CUDA device")
-    for t in (exps, err, page_table, row_start, kv_len):
-        if t.get_device() != dev:
-            _kv8_refuse("every tensor must be on the cache's device")
-    if codes.dtype != torch.uint8 or exps.dtype != torch.uint8 or err.dtype != torch.int32:
+    if (exps.get_device() != dev or err.get_device() != dev or page_table.get_device() != dev or
+            row_start.get_device() != dev or kv_len.get_device() != dev):
+        _kv8_refuse("every tensor must be on the cache's device")
+    if codes.dtype is not u8 or exps.dtype is not u8 or err.dtype is not i32:
         _kv8_refuse("codes and exps must be uint8, err int32")
-    if codes.dim() != 5 or codes.shape[1] != 2 or not codes.is_contiguous() or not exps.is_contiguous():
+    shape = codes.shape
+    if len(shape) != 5 or shape[1] != 2 or not codes.is_contiguous() or not exps.is_contiguous():
         _kv8_refuse("codes must be a contiguous [n_pages, 2, heads, page_tokens, head_dim] tensor")
-    n, _, heads, page, hd = codes.shape
-    if exps.shape != (n, heads, page, 2) or err.numel() < 1:
+    if exps.shape != (shape[0], shape[2], shape[3], 2) or err.numel() < 1:
         _kv8_refuse("exps must be [n_pages, heads, page_tokens, 2]")
-    if page_table.dtype != torch.int32 or row_start.dtype != torch.int32 or kv_len.dtype != torch.int32:
+    if page_table.dtype is not i32 or row_start.dtype is not i32 or kv_len.dtype is not i32:
         _kv8_refuse("page_table, row_start and kv_len must be int32")
-    nseq = kv_len.shape[0]
-    if page_table.dim() != 2 or kv_len.dim() != 1 or row_start.shape != (nseq + 1,) or page_table.shape[0] < nseq:
+    nseq, table = kv_len.numel(), page_table.shape
+    if (len(table) != 2 or table[0] < nseq or kv_len.dim() != 1 or row_start.dim() != 1 or
+            row_start.numel() != nseq + 1):
         _kv8_refuse("page_table [seqs, entries], row_start [seqs + 1] and kv_len [seqs] do not agree")
     if not (page_table.is_contiguous() and row_start.is_contiguous() and kv_len.is_contiguous()):
         _kv8_refuse("page_table, row_start and kv_len must be contiguous")
-    return dev, (n, page, heads, hd), nseq
+    return dev, shape, nseq, table[1]
 
 
-def _kv8_call(dev: int, stream, what: str, fn, *args):
+def _kv8_call(dev: int, stream, current: int, raw_stream, what: str, fn, *args):
     """fn(*args, stream) on device `dev`'s current stream, or on `stream`."""
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        handle = raw_stream(dev)
     elif stream.device_index != dev:
         _kv8_refuse("the stream belongs to another device")
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, stream.cuda_stream)
     else:
+        handle = stream.cuda_stream
+    if current == dev:
+        st = fn(*args, handle)
+    else:
+        import torch
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, handle)
     if st != DF_OK:
         raise DfError(st, what)
 
@@ -661,9 +674,9 @@ def _kv8_empty(shape, dtype, dev: int, stream):
     """An output tensor that belongs to the stream the call runs on."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def kv8_write(cache: KV8Cache, k, v, page_table, row_start, kv_len, stream=None):
@@ -672,41 +685,50 @@ def kv8_write(cache: KV8Cache, k, v, page_table, row_start, kv_len, stream=None)
     fused projection); page_table [seqs, entries], row_start [seqs + 1],
     kv_len [seqs] int32: sequence s owns rows row_start[s]..row_start[s + 1] - 1,
     its last positions up to kv_len[s] - 1."""
-    import torch
-    dev, (n, page, heads, hd), nseq = _kv8_plan(cache, page_table, row_start, kv_len)
-    if k.get_device() != dev or v.get_device() != dev or k.dtype != v.dtype:
+    if cache.codes.get_device() < 0:
+        _kv8_refuse("the cache must be on a CUDA device")
+    u8, i32, bf16, f32, raw, current, fn, _, _ = _kv8_bind()
+    dev, (n, _, heads, page, hd), nseq, entries = _kv8_plan(cache, page_table, row_start, kv_len, u8, i32)
+    dtype, shape = k.dtype, k.shape
+    if k.get_device() != dev or v.get_device() != dev or dtype is not v.dtype:
         _kv8_refuse("k and v must be of one type, on the cache's device")
-    dt = DF_BF16 if k.dtype == torch.bfloat16 else DF_FP32 if k.dtype == torch.float32 else -1
-    if dt < 0 or k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (heads, hd):
+    dt = DF_BF16 if dtype is bf16 else DF_FP32 if dtype is f32 else -1
+    if dt < 0 or len(shape) != 3 or shape != v.shape or shape[1] != heads or shape[2] != hd:
         _kv8_refuse("k and v must be bf16 or fp32 [rows, heads, head_dim]")
     (ks, kh, kd), (vs, vh, vd) = k.stride(), v.stride()
-    rows = k.shape[0]
-    if rows and ((kh, kd) != (hd, 1) and heads > 1 or (vh, vd) != (hd, 1) and heads > 1 or kd != 1 or vd != 1):
+    rows = shape[0]
+    if rows and (kd != 1 or vd != 1 or heads > 1 and (kh != hd or vh != hd)):
         _kv8_refuse("the heads of a row must be contiguous")
     if rows < 2:  # a single row's stride says nothing
         ks = vs = heads * hd
-    _kv8_call(dev, stream, "df_op_kv8_write", lib().df_op_kv8_write, k.data_ptr(), v.data_ptr(), dt, rows, ks, vs,
-              cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(),
-              page_table.shape[1], row_start.data_ptr(), kv_len.data_ptr(), nseq, cache.err.data_ptr())
+    _kv8_call(dev, stream, current(), raw, "df_op_kv8_write", fn, k.data_ptr(), v.data_ptr(), dt, rows, ks, vs,
+              cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(), entries,
+              row_start.data_ptr(), kv_len.data_ptr(), nseq, cache.err.data_ptr())
 
 
 def kv8_read(cache: KV8Cache, page_table, row_start, kv_len, rows: int, dtype=None, k=None, v=None, stream=None):
     """Read rows back (df_op_kv8_read): (k, v), each [rows, Hkv, head_dim] in
     `dtype` (bf16, the default, or fp32).  k and v may be given."""
-    import torch
-    dev, (n, page, heads, hd), nseq = _kv8_plan(cache, page_table, row_start, kv_len)
-    dtype = dtype if dtype is not None else k.dtype if k is not None else torch.bfloat16
-    dt = DF_BF16 if dtype == torch.bfloat16 else DF_FP32 if dtype == torch.float32 else -1
-    if dt < 0 or rows < 0:
+    if cache.codes.get_device() < 0:
+        _kv8_refuse("the cache must be on a CUDA device")
+    u8, i32, bf16, f32, raw, current, _, fn, _ = _kv8_bind()
+    dev, (n, _, heads, page, hd), nseq, entries = _kv8_plan(cache, page_table, row_start, kv_len, u8, i32)
+    dtype = dtype if dtype is not None else k.dtype if k is not None else bf16
+    dt = DF_BF16 if dtype is bf16 else DF_FP32 if dtype is f32 else -1
+    if dt < 0 or not 0 <= rows <= _I32_MAX:
         _kv8_refuse("rows must not be negative, and the type bf16 or fp32")
-    k = _kv8_empty((rows, heads, hd), dtype, dev, stream) if k is None else k
-    v = _kv8_empty((rows, heads, hd), dtype, dev, stream) if v is None else v
-    for t in (k, v):
-        if t.get_device() != dev or t.dtype != dtype or t.shape != (rows, heads, hd) or not t.is_contiguous():
-            _kv8_refuse("k and v must be contiguous [rows, heads, head_dim] tensors of the type")
-    _kv8_call(dev, stream, "df_op_kv8_read", lib().df_op_kv8_read, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
-              page, heads, hd, page_table.data_ptr(), page_table.shape[1], row_start.data_ptr(), kv_len.data_ptr(),
-              nseq, rows, dt, k.data_ptr(), v.data_ptr(), cache.err.data_ptr())
+    shape = (rows, heads, hd)
+    if k is None:
+        k = _kv8_empty(shape, dtype, dev, stream)
+    elif k.get_device() != dev or k.dtype is not dtype or k.shape != shape or not k.is_contiguous():
+        _kv8_refuse("k must be a contiguous [rows, heads, head_dim] tensor of the type")
+    if v is None:
+        v = _kv8_empty(shape, dtype, dev, stream)
+    elif v.get_device() != dev or v.dtype is not dtype or v.shape != shape or not v.is_contiguous():
+        _kv8_refuse("v must be a contiguous [rows, heads, head_dim] tensor of the type")
+    _kv8_call(dev, stream, current(), raw, "df_op_kv8_read", fn, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
+              page, heads, hd, page_table.data_ptr(), entries, row_start.data_ptr(), kv_len.data_ptr(), nseq, rows,
+              dt, k.data_ptr(), v.data_ptr(), cache.err.data_ptr())
     return k, v
 
 
@@ -719,26 +741,39 @@ def attention_kv8(q, cache: KV8Cache, page_table, row_start, kv_len, max_rows: i
     (the last `window` of them if window > 0), else every cached position of
     its sequence; lse: fp32 [rows, Hq], filled if given, or True to make one.
     Returns (out, lse)."""
-    import torch
-    dev, (n, page, heads, hd), nseq = _kv8_plan(cache, page_table, row_start, kv_len)
-    if q.get_device() != dev or q.dtype != torch.bfloat16 or q.dim() != 2 or q.shape[1] % hd:
+    if cache.codes.get_device() < 0:
+        _kv8_refuse("the cache must be on a CUDA device")
+    u8, i32, bf16, f32, raw, current, _, _, fn = _kv8_bind()
+    dev, (n, _, heads, page, hd), nseq, entries = _kv8_plan(cache, page_table, row_start, kv_len, u8, i32)
+    shape = q.shape
+    if q.get_device() != dev or q.dtype is not bf16 or len(shape) != 2 or shape[1] % hd:
         _kv8_refuse("q must be bf16 [rows, Hq * head_dim] on the cache's device")
-    rows, width = q.shape
+    rows, width = shape
     hq = width // hd
-    out = _kv8_empty((rows, width), torch.bfloat16, dev, stream) if out is None else out
-    if out.get_device() != dev or out.dtype != torch.bfloat16 or out.shape != (rows, width):
+    if out is None:
+        out = _kv8_empty(shape, bf16, dev, stream)
+    elif out.get_device() != dev or out.dtype is not bf16 or out.shape != shape:
         _kv8_refuse("out must be bf16 and shaped as q")
-    qs, os_ = (q.stride(0), out.stride(0)) if rows > 1 else (width, width)
-    if rows and (q.stride(1) != 1 or out.stride(1) != 1):
+    (qs, qd), (os_, od) = q.stride(), out.stride()
+    if rows and (qd != 1 or od != 1):
         _kv8_refuse("the elements of a row must be contiguous")
-    if lse is True:
-        lse = _kv8_empty((rows, hq), torch.float32, dev, stream)
-    if lse is not None and (lse.get_device() != dev or lse.dtype != torch.float32 or lse.shape != (rows, hq) or
-                            not lse.is_contiguous()):
-        _kv8_refuse("lse must be a contiguous fp32 [rows, Hq] tensor")
-    _kv8_call(dev, stream, "df_op_attention_kv8", lib().df_op_attention_kv8, q.data_ptr(), qs, out.data_ptr(), os_,
-              lse.data_ptr() if lse is not None else None, rows, hq, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
-              page, heads, hd, page_table.data_ptr(), page_table.shape[1], row_start.data_ptr(), kv_len.data_ptr(),
-              nseq, min(int(max_rows), rows), min(int(max_len), _I32_MAX), scale if scale is not None else hd ** -0.5,
-              1 if causal else 0, min(int(window), _I32_MAX), cluster_ctas, cache.err.data_ptr())
+    if rows < 2:
+        qs = os_ = width
+    lse_ptr = None
+    if lse is not None:
+        if lse is True:
+            lse = _kv8_empty((rows, hq), f32, dev, stream)
+        elif (lse.get_device() != dev or lse.dtype is not f32 or lse.shape != (rows, hq) or
+              not lse.is_contiguous()):
+            _kv8_refuse("lse must be a contiguous fp32 [rows, Hq] tensor")
+        lse_ptr = lse.data_ptr()
+    if max_rows > rows:
+        max_rows = rows
+    if max_len > _I32_MAX or window > _I32_MAX:
+        max_len, window = min(max_len, _I32_MAX), min(window, _I32_MAX)
+    _kv8_call(dev, stream, current(), raw, "df_op_attention_kv8", fn, q.data_ptr(), qs, out.data_ptr(), os_, lse_ptr,
+              rows, hq, cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(),
+              entries, row_start.data_ptr(), kv_len.data_ptr(), nseq, int(max_rows), int(max_len),
+              scale if scale is not None else hd ** -0.5, 1 if causal else 0, int(window), cluster_ctas,
+              cache.err.data_ptr())
     return out, lse
