@@ -64,6 +64,7 @@ struct Kv8Attn {
   long long qs, os;  // row strides (elements)
   int q_heads, group, max_rows, causal, window, tiles;
   float scale_log2;
+  unsigned long long per_page;  // 2^32 / (groups of 16 tokens of a page), rounded up
 };
 
 constexpr int K8_CHUNK = 128;     // keys per chunk: one per tensor-memory lane
@@ -425,20 +426,29 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const unsigned n_mine = c_end > c_first ? (c_end - c_first + C - 1) / C : 0;
 
   bool ok = true;
-  // Producer, chunk i: lanes 0-7 bring its groups of 16 keys, lanes 8-15 its
-  // groups of values, lanes 16-23 the exponents.
-  auto produce = [&](unsigned i) {
-    const int st = i % STAGES, gr = lane & 7, pos = (c_first + (int)i * C) * K8_CHUNK + gr * 16;
-    int page = -1;
-    if (lane < 24 && pos < len) {
-      page = g.page_table[(size_t)s * g.pt_stride + pos / g.page_tokens];
-      if (page < 0 || page >= g.n_pages) {
-        page = -1;
-        flag_error(g.err, ERR_BOUNDS);
-      }
+  // Producer: lanes 0-7 bring a chunk's groups of 16 keys, lanes 8-15 its
+  // groups of values, lanes 16-23 the exponents.  The page of the lane's group
+  // is looked up a chunk ahead.
+  struct Place {
+    int page, slot;  // page -1: none
+  };
+  auto place = [&](unsigned i) {
+    Place p{-1, 0};
+    if (i < n_mine && lane < 24) {
+      const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + (lane & 7);
+      const unsigned entry = (unsigned)(((unsigned long long)group * a.per_page) >> 32);  // group / groups of a page
+      p.slot = (int)(group * 16 - entry * g.page_tokens);
+      if ((int)group * 16 < len) p.page = g.page_table[(size_t)s * g.pt_stride + entry];
     }
-    const uint32_t live = __ballot_sync(0xffffffffu, page >= 0) & 0xffu;
-    const int slot = pos % g.page_tokens;
+    return p;
+  };
+  auto produce = [&](unsigned i, Place p) {
+    const int st = i % STAGES, gr = lane & 7;
+    if (p.page >= g.n_pages || (p.page < 0 && lane < 8 && (c_first + (int)i * C) * K8_CHUNK + gr * 16 < len)) {
+      p.page = -1;
+      flag_error(g.err, ERR_BOUNDS);
+    }
+    const uint32_t live = __ballot_sync(0xffffffffu, p.page >= 0) & 0xffu;
     if (i >= STAGES) {
       k8_wait(bars + L::EK + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
       ok = __all_sync(0xffffffffu, ok);
@@ -446,9 +456,9 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
     }
     if (lane == 0) k8_arrive_tx(bars + L::FK + st * 8, __popc(live) * 16 * HD);
     __syncwarp();
-    if (lane < 8 && page >= 0)
-      k8_load_keys(smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, slot,
-                   (page * 2) * g.heads + head);
+    if (lane < 8 && p.page >= 0)
+      k8_load_keys(smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, p.slot,
+                   (p.page * 2) * g.heads + head);
     if (i >= STAGES) {
       k8_wait(bars + L::EV + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
       ok = __all_sync(0xffffffffu, ok);
@@ -459,12 +469,13 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       k8_arrive_tx(bars + L::FV + st * 8, __popc(live) * (16 * HD + 32));
     }
     __syncwarp();
-    if (lane >= 8 && lane < 16 && page >= 0)
-      k8_load_bytes(smb + (L::VOFF + st * L::TILE + gr * 16 * HD),
-                    g.codes + kv8_code_at(g, page, 1, head) + (size_t)slot * HD, 16 * HD, bars + L::FV + st * 8);
-    if (lane >= 16 && page >= 0)
-      k8_load_bytes(smb + (L::EOFF + st * K8_CHUNK * 2 + gr * 32), g.exps + kv8_exp_at(g, page, head, slot), 32,
-                    bars + L::FV + st * 8);
+    if (lane >= 8 && p.page >= 0) {
+      const bool ex = lane >= 16;
+      const uint8_t* src = ex ? g.exps + kv8_exp_at(g, p.page, head, p.slot)
+                              : g.codes + kv8_code_at(g, p.page, 1, head) + (size_t)p.slot * HD;
+      k8_load_bytes(smb + (ex ? L::EOFF + st * K8_CHUNK * 2 + gr * 32 : L::VOFF + st * L::TILE + gr * 16 * HD), src,
+                    ex ? 32 : 16 * HD, bars + L::FV + st * 8);
+    }
   };
 
   // Q: LPR lanes to a row, 8 elements each; the loads start here.
@@ -488,7 +499,12 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
-    for (unsigned i = 0; i < STAGES && i < n_mine; ++i) produce(i);
+    Place p[STAGES];
+#pragma unroll
+    for (unsigned i = 0; i < STAGES; ++i) p[i] = place(i);  // all look-ups first
+#pragma unroll
+    for (unsigned i = 0; i < STAGES; ++i)
+      if (i < n_mine) produce(i, p[i]);
   } else if (warp == ISSUER) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(k8_addr(&s_tmem)),
                  "n"(L::COLS)
@@ -525,7 +541,12 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const uint32_t tmem = s_tmem;
 
   if (warp == PRODUCER) {
-    for (unsigned i = STAGES; ok && i < n_mine; ++i) produce(i);
+    Place next = place(STAGES);
+    for (unsigned i = STAGES; ok && i < n_mine; ++i) {
+      const Place p = next;
+      next = place(i + 1);
+      produce(i, p);
+    }
     // The other warps wait for every tile, so no copy is in flight when they
     // are done; if a wait ran out, give the copies issued the same time to land.
     if (!ok)
@@ -996,6 +1017,8 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   a.max_rows = max_rows < rows ? max_rows : rows;
   a.causal = causal;
   a.window = window;
+  // exact for a group number below 2^26 and at most 64 groups to a page
+  a.per_page = ((1ull << 32) + page_tokens / 16 - 1) / (page_tokens / 16);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   // the narrowest tile that holds a sequence's rows, or the widest
   const long long wanted = (long long)a.max_rows * a.group;
