@@ -119,8 +119,13 @@ __device__ __forceinline__ void k8_arrive_warp(uint32_t bar) {
       "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void k8_arrive_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+__device__ __forceinline__ void k8_arrive_tx(uint32_t one, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+      "r"(bytes), "r"(one)
+      : "memory");
 }
 __device__ __forceinline__ bool k8_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -188,18 +193,38 @@ __device__ __forceinline__ void k8_sts8(uint32_t addr, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// 16 key rows (16 x HD bytes) of slab (page, k, head) into swizzled rows.
-__device__ __forceinline__ void k8_load_keys(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int slab) {
+// One lane of the converged warp.  The instructions below that one thread
+// issues are executed by the whole warp and predicated on it, so that their
+// operands stay in uniform registers (under a divergent branch each of them
+// costs its issuing thread about 80 cycles of register moves).
+__device__ __forceinline__ uint32_t k8_elect() {
+  uint32_t r;
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(slot), "r"(slab)
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r;
+}
+
+// 16 key rows (16 x HD bytes) of slab (page, k, head) into swizzled rows.
+__device__ __forceinline__ void k8_load_keys(uint32_t one, uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot,
+                                             int slab) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(slot), "r"(slab), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void k8_load_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void k8_load_bytes(uint32_t one, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "r"(one)
+      : "memory");
 }
 
 // Shared-memory descriptors.  Rows of 128 bytes in the 128-byte swizzle (8-row
@@ -217,25 +242,32 @@ __host__ __device__ constexpr uint32_t k8_idesc(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 // D = (acc) D + A . B, e4m3, both in shared memory.
-__device__ __forceinline__ void k8_mma_codes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void k8_mma_codes(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
       : "memory");
 }
 // D = (acc) D + A . B, f16, A in tensor memory.
-__device__ __forceinline__ void k8_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void k8_mma(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
       : "memory");
 }
-__device__ __forceinline__ void k8_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void k8_commit(uint32_t one, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(one)
+      : "memory");
 }
 
 // W columns (8, 16 or 32) of the thread's tensor-memory lane.
@@ -396,7 +428,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   __shared__ float s_red[4][N];
 
   const Kv8Geom& g = a.g;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
   const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
   const int G = a.group;
@@ -426,16 +458,15 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const unsigned n_mine = c_end > c_first ? (c_end - c_first + C - 1) / C : 0;
 
   bool ok = true;
-  // Producer: lanes 0-7 bring a chunk's groups of 16 keys, lanes 8-15 its
-  // groups of values, lanes 16-23 the exponents.  The page of the lane's group
-  // is looked up a chunk ahead.
+  // Producer: a chunk's groups of 16 keys, its groups of values and their
+  // exponents.  The pages are looked up a chunk ahead, by lanes 0-7.
   struct Place {
     int page, slot;  // page -1: none
   };
   auto place = [&](unsigned i) {
     Place p{-1, 0};
-    if (i < n_mine && lane < 24) {
-      const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + (lane & 7);
+    if (i < n_mine && lane < 8) {
+      const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + lane;
       const unsigned entry = (unsigned)(((unsigned long long)group * a.per_page) >> 32);  // group / groups of a page
       p.slot = (int)(group * 16 - entry * g.page_tokens);
       if ((int)group * 16 < len) p.page = g.page_table[(size_t)s * g.pt_stride + entry];
@@ -443,39 +474,49 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
     return p;
   };
   auto produce = [&](unsigned i, Place p) {
-    const int st = i % STAGES, gr = lane & 7;
-    if (p.page >= g.n_pages || (p.page < 0 && lane < 8 && (c_first + (int)i * C) * K8_CHUNK + gr * 16 < len)) {
+    const int st = i % STAGES, key0 = (c_first + (int)i * C) * K8_CHUNK;
+    if (p.page >= g.n_pages || (p.page < 0 && lane < 8 && key0 + lane * 16 < len)) {
       p.page = -1;
       flag_error(g.err, ERR_BOUNDS);
     }
     const uint32_t live = __ballot_sync(0xffffffffu, p.page >= 0) & 0xffu;
+    const uint32_t one = k8_elect();
+    int slab[8], slot[8];
+#pragma unroll
+    for (int gr = 0; gr < 8; ++gr) {
+      slab[gr] = __shfl_sync(0xffffffffu, p.page, gr) * 2 * g.heads + head;
+      slot[gr] = __shfl_sync(0xffffffffu, p.slot, gr);
+    }
     if (i >= STAGES) {
       k8_wait(bars + L::EK + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
     }
-    if (lane == 0) k8_arrive_tx(bars + L::FK + st * 8, __popc(live) * 16 * HD);
-    __syncwarp();
-    if (lane < 8 && p.page >= 0)
-      k8_load_keys(smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, p.slot,
-                   (p.page * 2) * g.heads + head);
+    k8_arrive_tx(one, bars + L::FK + st * 8, __popc(live) * 16 * HD);
+#pragma unroll
+    for (int gr = 0; gr < 8; ++gr)
+      if (live >> gr & 1)
+        k8_load_keys(one, smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, slot[gr], slab[gr]);
     if (i >= STAGES) {
       k8_wait(bars + L::EV + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
     }
-    if (lane == 0) {
-      s_live[st] = (int)live;
-      k8_arrive_tx(bars + L::FV + st * 8, __popc(live) * (16 * HD + 32));
-    }
+    if (lane == 0) s_live[st] = (int)live;
     __syncwarp();
-    if (lane >= 8 && p.page >= 0) {
-      const bool ex = lane >= 16;
-      const uint8_t* src = ex ? g.exps + kv8_exp_at(g, p.page, head, p.slot)
-                              : g.codes + kv8_code_at(g, p.page, 1, head) + (size_t)p.slot * HD;
-      k8_load_bytes(smb + (ex ? L::EOFF + st * K8_CHUNK * 2 + gr * 32 : L::VOFF + st * L::TILE + gr * 16 * HD), src,
-                    ex ? 32 : 16 * HD, bars + L::FV + st * 8);
-    }
+    k8_arrive_tx(one, bars + L::FV + st * 8, __popc(live) * (16 * HD + 32));
+    const uint8_t* codes = g.codes + (size_t)g.heads * g.page_tokens * HD;  // the first page's values
+#pragma unroll
+    for (int gr = 0; gr < 8; ++gr)
+      if (live >> gr & 1)
+        k8_load_bytes(one, smb + (L::VOFF + st * L::TILE + gr * 16 * HD),
+                      codes + ((size_t)slab[gr] * g.page_tokens + slot[gr]) * HD, 16 * HD, bars + L::FV + st * 8);
+#pragma unroll
+    for (int gr = 0; gr < 8; ++gr)
+      if (live >> gr & 1)
+        k8_load_bytes(one, smb + (L::EOFF + st * K8_CHUNK * 2 + gr * 32),
+                      g.exps + ((size_t)((slab[gr] + head) >> 1) * g.page_tokens + slot[gr]) * 2, 32,
+                      bars + L::FV + st * 8);
   };
 
   // Q: LPR lanes to a row, 8 elements each; the loads start here.
@@ -538,7 +579,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   }
   __syncthreads();
   k8_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
   if (warp == PRODUCER) {
     Place next = place(STAGES);
@@ -558,7 +599,8 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
     __syncwarp();
   } else if (warp == ISSUER) {
     asm volatile("bar.sync 10, %0;" ::"n"(CT + 32) : "memory");  // Q is in shared memory
-    if (lane == 0 && n_mine > 0) {
+    if (n_mine > 0) {
+      const uint32_t one = k8_elect();
       const uint64_t kd = k8_desc<HD>(smb + (L::KOFF)), qd = k8_desc<HD>(smb + (L::QOFF)),
                      pd = k8_desc<128>(smb + (L::POFF), K8_CHUNK * 128);
       // S^T of chunk i; its key tile is free when that is done
@@ -568,11 +610,11 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
         k8_fence_after();
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)  // the queries' high halves, then the low ones
-          k8_mma_codes(tmem + L::SCOL, kd + (uint64_t)((st * L::TILE + kk % (HD / 32) * 32) >> 4),
+          k8_mma_codes(one, tmem + L::SCOL, kd + (uint64_t)((st * L::TILE + kk % (HD / 32) * 32) >> 4),
                        qd + (uint64_t)((kk / (HD / 32) * N * HD + kk % (HD / 32) * 32) >> 4), k8_idesc(N, false),
                        kk > 0);
-        k8_commit(bars + L::SS);
-        k8_commit(bars + L::EK + st * 8);
+        k8_commit(one, bars + L::SS);
+        k8_commit(one, bars + L::EK + st * 8);
       };
       scores(0);
       for (unsigned i = 0; i < n_mine; ++i) {
@@ -584,9 +626,9 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
         k8_fence_after();
 #pragma unroll
         for (int kk = 0; kk < K8_CHUNK / 16; ++kk)
-          k8_mma(tmem + L::OCOL, tmem + L::VCOL + (i & 1) * 64 + 8 * kk, pd + (uint64_t)((kk * 2048) >> 4),
+          k8_mma(one, tmem + L::OCOL, tmem + L::VCOL + (i & 1) * 64 + 8 * kk, pd + (uint64_t)((kk * 2048) >> 4),
                  k8_idesc(N, true), i > 0 || kk > 0);
-        k8_commit(bars + L::OU);
+        k8_commit(one, bars + L::OU);
       }
       // every product has finished before tensor memory is freed
       bool done = true;
