@@ -37,7 +37,7 @@
 //
 // Roles: GROUPS groups of four warps widen values and run the softmax, each
 // group on its N / GROUPS query rows (a thread's columns of S) and its share
-// of the chunk's values; one warp stages keys, values and exponents by TMA;
+// of the chunk's values; three warps stage keys, values and exponents by TMA;
 // one issues the tensor-core instructions and owns the tensor memory.  S
 // leaves tensor memory for registers at once, so the next chunk's S is
 // computed while the softmax of this one runs.  Tiles of up to 64 rows run two
@@ -79,8 +79,12 @@ struct K8 {
   static constexpr int GROUPS = N == 128 ? 4 : 2;
   static constexpr int W = N / GROUPS;                  // query rows (columns of S) of a thread
   static constexpr int CTHREADS = 128 * GROUPS;         // threads that widen and run the softmax
-  static constexpr int THREADS = CTHREADS + 64;
+  static constexpr int THREADS = CTHREADS + 128;        // and four warps that stage and issue
   static constexpr int PER_SM = N == 128 ? 1 : 2;       // CTAs on an SM
+  // Registers of a thread: the kernel's at launch, then those of the softmax
+  // and of the staging warps (their sum stays within the launch's)
+  static constexpr int REGS = 65536 / PER_SM / THREADS / 16 * 16, CREGS = N == 128 ? 104 : 96, AREGS = N == 128 ? 64 : 48;
+  static_assert(CTHREADS * CREGS + 128 * AREGS <= THREADS * REGS, "registers of the launch");
   static constexpr int COLS = 512 / PER_SM;             // tensor-memory columns of a CTA:
   static constexpr int VCOL = 0;                        // widened values of an even and an odd chunk (two to a column),
   static constexpr int SCOL = 128;                      // S,
@@ -138,7 +142,8 @@ __device__ __forceinline__ bool k8_test(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-__device__ __noinline__ bool k8_wait_slow(uint32_t bar, uint32_t parity, bool ok, int* err) {
+// (Inline: the register split does not allow calls.)
+__device__ __forceinline__ bool k8_wait_slow(uint32_t bar, uint32_t parity, bool ok, int* err) {
   if (!ok) return false;
   const unsigned long long t0 = device_ns();
   for (uint32_t it = 1; it < (1u << 30); ++it) {
@@ -208,22 +213,21 @@ __device__ __forceinline__ uint32_t k8_elect() {
 }
 
 // 16 key rows (16 x HD bytes) of slab (page, k, head) into swizzled rows.
-__device__ __forceinline__ void k8_load_keys(uint32_t one, uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot,
-                                             int slab) {
+__device__ __forceinline__ void k8_load_keys(uint32_t dst, const CUtensorMap* map, uint32_t bar, int slot, int slab) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %6, 0;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
       "@p cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];\n}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(slot), "r"(slab), "r"(one)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(slot), "r"(slab)
       : "memory");
 }
-__device__ __forceinline__ void k8_load_bytes(uint32_t one, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+__device__ __forceinline__ void k8_load_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
       "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}\n" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "r"(one)
+      "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
   const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
   const int G = a.group;
-  constexpr int PRODUCER = CT / 32, ISSUER = PRODUCER + 1;
+  constexpr int ISSUER = CT / 32, KEYS = ISSUER + 1, VALUES = ISSUER + 2;  // and exponents
 
   // The tile's rows; every CTA of a cluster takes the same way out.
   Kv8Seq sq;
@@ -458,13 +462,14 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const unsigned n_mine = c_end > c_first ? (c_end - c_first + C - 1) / C : 0;
 
   bool ok = true;
-  // Producer: a chunk's groups of 16 keys, its groups of values and their
-  // exponents.  The pages are looked up a chunk ahead, by lanes 0-7.
+  // Staging: a chunk's 8 groups of 16 keys, of values and of exponents are 24
+  // copies, each of which costs the warp that issues it about 100 cycles, so
+  // three warps share them.  Pages are looked up a chunk ahead, in lanes 0-7.
   struct Place {
-    int page, slot;  // page -1: none
+    int page, slot;  // page -2: no such group
   };
   auto place = [&](unsigned i) {
-    Place p{-1, 0};
+    Place p{-2, 0};
     if (i < n_mine && lane < 8) {
       const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + lane;
       const unsigned entry = (unsigned)(((unsigned long long)group * a.per_page) >> 32);  // group / groups of a page
@@ -473,50 +478,54 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
     }
     return p;
   };
-  auto produce = [&](unsigned i, Place p) {
-    const int st = i % STAGES, key0 = (c_first + (int)i * C) * K8_CHUNK;
-    if (p.page >= g.n_pages || (p.page < 0 && lane < 8 && key0 + lane * 16 < len)) {
-      p.page = -1;
+  // (apart from the look-up, which would otherwise be waited for at once)
+  auto checked = [&](Place p) {
+    if (p.page != -2 && (p.page < 0 || p.page >= g.n_pages)) {
+      p.page = -2;
       flag_error(g.err, ERR_BOUNDS);
     }
-    const uint32_t live = __ballot_sync(0xffffffffu, p.page >= 0) & 0xffu;
-    const uint32_t one = k8_elect();
-    int slab[8], slot[8];
+    return p;
+  };
+  // Everything a copy needs is in registers before the wait for its stage: the
+  // copies then follow one another without waiting for a shuffle or a product.
+  auto produce = [&](unsigned i, Place p, uint32_t one) {
+    const int st = i % STAGES;
+    const uint32_t live = __ballot_sync(0xffffffffu, p.page >= 0);
+    if (warp == KEYS) {
+      int slab[8], slot[8];
 #pragma unroll
-    for (int gr = 0; gr < 8; ++gr) {
-      slab[gr] = __shfl_sync(0xffffffffu, p.page, gr) * 2 * g.heads + head;
-      slot[gr] = __shfl_sync(0xffffffffu, p.slot, gr);
+      for (int gr = 0; gr < 8; ++gr) {
+        slab[gr] = __shfl_sync(0xffffffffu, p.page * 2 * g.heads + head, gr);
+        slot[gr] = __shfl_sync(0xffffffffu, p.slot, gr);
+      }
+      if (i >= STAGES) k8_wait(bars + L::EK + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      k8_arrive_tx(one, bars + L::FK + st * 8, __popc(live) * 16 * HD);
+#pragma unroll
+      for (int gr = 0; gr < 8; ++gr)
+        if (live >> gr & 1)
+          k8_load_keys(smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, slot[gr], slab[gr]);
+    } else {
+      // values are the second plane of a page; exponents of both kinds lie together
+      const bool values = warp == VALUES;
+      const unsigned long long at =
+          ((unsigned long long)(values ? p.page * 2 + 1 : p.page) * g.heads + head) * g.page_tokens + p.slot;
+      const unsigned long long lane_src =
+          values ? (unsigned long long)g.codes + at * HD : (unsigned long long)g.exps + at * 2;
+      const uint32_t bytes = values ? 16 * HD : 32;
+      const uint32_t dst = smb + (values ? L::VOFF + st * L::TILE : L::EOFF + st * K8_CHUNK * 2);
+      unsigned long long src[8];
+#pragma unroll
+      for (int gr = 0; gr < 8; ++gr) src[gr] = __shfl_sync(0xffffffffu, lane_src, gr);
+      if (i >= STAGES) k8_wait(bars + L::EV + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      if (values && lane == 0) s_live[st] = (int)live;
+      __syncwarp();
+      k8_arrive_tx(one, bars + L::FV + st * 8, __popc(live) * bytes);
+#pragma unroll
+      for (int gr = 0; gr < 8; ++gr)
+        if (live >> gr & 1) k8_load_bytes(dst + gr * bytes, (const void*)src[gr], bytes, bars + L::FV + st * 8);
     }
-    if (i >= STAGES) {
-      k8_wait(bars + L::EK + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-    }
-    k8_arrive_tx(one, bars + L::FK + st * 8, __popc(live) * 16 * HD);
-#pragma unroll
-    for (int gr = 0; gr < 8; ++gr)
-      if (live >> gr & 1)
-        k8_load_keys(one, smb + (L::KOFF + st * L::TILE + gr * 16 * HD), &kmap, bars + L::FK + st * 8, slot[gr], slab[gr]);
-    if (i >= STAGES) {
-      k8_wait(bars + L::EV + st * 8, (i / STAGES - 1) & 1u, ok, g.err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-    }
-    if (lane == 0) s_live[st] = (int)live;
-    __syncwarp();
-    k8_arrive_tx(one, bars + L::FV + st * 8, __popc(live) * (16 * HD + 32));
-    const uint8_t* codes = g.codes + (size_t)g.heads * g.page_tokens * HD;  // the first page's values
-#pragma unroll
-    for (int gr = 0; gr < 8; ++gr)
-      if (live >> gr & 1)
-        k8_load_bytes(one, smb + (L::VOFF + st * L::TILE + gr * 16 * HD),
-                      codes + ((size_t)slab[gr] * g.page_tokens + slot[gr]) * HD, 16 * HD, bars + L::FV + st * 8);
-#pragma unroll
-    for (int gr = 0; gr < 8; ++gr)
-      if (live >> gr & 1)
-        k8_load_bytes(one, smb + (L::EOFF + st * K8_CHUNK * 2 + gr * 32),
-                      g.exps + ((size_t)((slab[gr] + head) >> 1) * g.page_tokens + slot[gr]) * 2, 32,
-                      bars + L::FV + st * 8);
   };
 
   // Q: LPR lanes to a row, 8 elements each; the loads start here.
@@ -524,12 +533,12 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const int sub = threadIdx.x % LPR;
   uint4 qw[QPASS];
 
-  if (warp == PRODUCER) {
-    if (lane == 0) {
+  if (warp > ISSUER) {
+    if (warp == KEYS && lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
       for (int i = 0; i < STAGES; ++i) {
         k8_bar_init(bars + L::FK + i * 8, 1);
-        k8_bar_init(bars + L::FV + i * 8, 1);
+        k8_bar_init(bars + L::FV + i * 8, 2);
         k8_bar_init(bars + L::EK + i * 8, 1);
         k8_bar_init(bars + L::EV + i * 8, CT / 32);
       }
@@ -539,13 +548,15 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       k8_bar_init(bars + L::OU, 1);        // O updated
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncwarp();
+    // the first stages start before the other warps are ready
     Place p[STAGES];
 #pragma unroll
-    for (unsigned i = 0; i < STAGES; ++i) p[i] = place(i);  // all look-ups first
+    for (unsigned i = 0; i < STAGES; ++i) p[i] = place(i);
+    const uint32_t one = k8_elect();
+    asm volatile("bar.sync 11, 96;" ::: "memory");
 #pragma unroll
     for (unsigned i = 0; i < STAGES; ++i)
-      if (i < n_mine) produce(i, p[i]);
+      if (i < n_mine) produce(i, checked(p[i]), one);
   } else if (warp == ISSUER) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(k8_addr(&s_tmem)),
                  "n"(L::COLS)
@@ -581,26 +592,32 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   k8_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
 
-  if (warp == PRODUCER) {
+  if (warp >= ISSUER)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::AREGS));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::CREGS));
+
+  if (warp > ISSUER) {
+    const uint32_t one = k8_elect();
     Place next = place(STAGES);
-    for (unsigned i = STAGES; ok && i < n_mine; ++i) {
-      const Place p = next;
+    for (unsigned i = STAGES; i < n_mine; ++i) {
+      const Place p = checked(next);
       next = place(i + 1);
-      produce(i, p);
+      produce(i, p, one);
     }
     // The other warps wait for every tile, so no copy is in flight when they
     // are done; if a wait ran out, give the copies issued the same time to land.
-    if (!ok)
+    if (!__all_sync(0xffffffffu, ok))
       for (int b = 0; b < STAGES; ++b)
-        for (uint32_t p = 0; p < 2; ++p) {
-          (void)(k8_test(bars + L::FK + b * 8, p) || k8_wait_slow(bars + L::FK + b * 8, p, true, g.err));
-          (void)(k8_test(bars + L::FV + b * 8, p) || k8_wait_slow(bars + L::FV + b * 8, p, true, g.err));
+        for (uint32_t q = 0; q < 2; ++q) {
+          (void)(k8_test(bars + L::FK + b * 8, q) || k8_wait_slow(bars + L::FK + b * 8, q, true, g.err));
+          (void)(k8_test(bars + L::FV + b * 8, q) || k8_wait_slow(bars + L::FV + b * 8, q, true, g.err));
         }
     __syncwarp();
   } else if (warp == ISSUER) {
+    const uint32_t one = k8_elect();
     asm volatile("bar.sync 10, %0;" ::"n"(CT + 32) : "memory");  // Q is in shared memory
     if (n_mine > 0) {
-      const uint32_t one = k8_elect();
       const uint64_t kd = k8_desc<HD>(smb + (L::KOFF)), qd = k8_desc<HD>(smb + (L::QOFF)),
                      pd = k8_desc<128>(smb + (L::POFF), K8_CHUNK * 128);
       // S^T of chunk i; its key tile is free when that is done
@@ -775,12 +792,13 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       if (k8_vote(group, pending || top > K8_SLACK + K8_BIAS)) {
         // M of some row moves: the chunk's largest term of every row.  A row
         // without a term so far takes it as M, another only if it is past the slack.
-        {
-          float v[W];
 #pragma unroll
-          for (int r = 0; r < W; ++r) v[r] = y[r];
-          const int base = k8_reduce<W>(v, [](float p, float q) { return fmaxf(p, q); });
-          s_red[warp & 3][w0 + base] = v[0];
+        for (int c = 0; c < W; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) v[r] = y[c + r];
+          const int base = k8_reduce<8>(v, [](float p, float q) { return fmaxf(p, q); });
+          s_red[warp & 3][w0 + c + base] = v[0];
         }
         k8_group_sync(group);
         bool wait = false;
@@ -902,7 +920,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   k8_cluster_sync();
   __shared__ float s_w[16][(N + 1) / 2], s_sum[(N + 1) / 2], s_top[(N + 1) / 2];
   const int mine = nr > rank ? (nr - rank + C - 1) / C : 0;
-  if (warp < PRODUCER) {
+  if (warp < ISSUER) {
     for (int r = threadIdx.x >> 4; r < mine; r += CT / 16) {  // 16 lanes to a row, one per rank
       const int row = rank + C * r, q = lane & 15;
       float m = -INFINITY, lq = 0.f;
