@@ -13,10 +13,11 @@
 // scale log2 e, and e_t = b_v - 127 added to the exponent).
 //
 // Keys go from the cache's bytes to the tensor core without a conversion: a
-// bf16 query has 8 bits, so a row brought to a largest magnitude in [128, 256)
-// by a power of two f_r is the sum of two e4m3 numbers of 4 bits each, exactly
-// for elements down to 2^-9 of the largest and to within 2^-17 of it below.
-// Both products go to one accumulator; the scores are taken times f_r.
+// bf16 query has 8 bits, so 32 q is the sum of two e4m3 numbers of 4 bits each,
+// exactly down to |q| = 2^-7 and to within 2^-15 below.  A row whose largest
+// magnitude is outside [1/4, 8) is first brought to [4, 8) by a power of two
+// f_r, and the scores of its tile are multiplied by f_r.  Both products go to
+// one accumulator.
 // Values need P at more than 8 bits and a wide range, so their product is f16:
 // a thread widens its head dim's codes of 128 values (the cache keeps values
 // transposed), exactly, and stores them to its own lane of tensor memory, the
@@ -71,6 +72,7 @@ constexpr int K8_CHUNK = 128;     // keys per chunk: one per tensor-memory lane
 constexpr int K8_SMS = 152;
 constexpr float K8_SLACK = 8.f;   // how far (log2) a term may pass M before M moves
 constexpr float K8_BIAS = 6.f;    // P = 2^K8_BIAS for a term at M
+constexpr float K8_QSCALE = 32.f; // queries are staged times this
 constexpr unsigned long long K8_WAIT_NS = 2000000000ull;
 
 // Shapes and shared memory of a CTA (offsets from a 1024-byte boundary).
@@ -425,6 +427,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(k8_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smb = k8_addr(sm), bars = smb + L::BOFF;
   __shared__ uint32_t s_tmem;
+  __shared__ int s_scaled;                                 // some row was brought into range
   __shared__ int s_live[STAGES];                           // groups of the chunk that hold positions
   __shared__ __align__(16) float s_m[N], s_neg[N], s_del[N], s_fac[N], s_qf[N], s_l[N];
   __shared__ __align__(16) int s_lo[N], s_hi[N];           // positions a row sees
@@ -535,6 +538,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
 
   if (warp > ISSUER) {
     if (warp == KEYS && lane == 0) {
+      s_scaled = 0;
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
       for (int i = 0; i < STAGES; ++i) {
         k8_bar_init(bars + L::FK + i * 8, 1);
@@ -668,8 +672,9 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       // the power of two taken out of the row (a row that holds no numbers becomes NaN)
-      const int out = min(max((int)(top >> 7) - 127 - 7, -119), 120);
-      const float by = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : kv8_pow2(-out);
+      const int e = (int)(top >> 7) - 127;
+      const int out = top == 0 || (e >= -2 && e < 3) ? 0 : min(max(e - 2, -114), 120);
+      const float by = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : K8_QSCALE * kv8_pow2(-out);
       float x[8], hi[8];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -693,11 +698,13 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
         k8_sts8(dst, ch);
         k8_sts8(dst + N * HD, cl);
         if (sub == 0) s_qf[r] = kv8_pow2(out);
+        if (out != 0) s_scaled = 1;
       }
     }
     k8_fence_smem();
     asm volatile("bar.arrive 10, %0;" ::"n"(CT + 32) : "memory");
-    k8_all_sync<CT>();  // s_qf
+    k8_all_sync<CT>();  // s_qf, s_scaled
+    const bool any_scaled = s_scaled != 0;
 
     float l[W];
 #pragma unroll
@@ -762,14 +769,17 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       k8_ld<W>(lane_base + L::SCOL + w0, y);
       k8_fence_before();
       k8_arrive_warp(bars + L::SR);  // the next chunk's scores may overwrite these
+      if (any_scaled)
+#pragma unroll
+        for (int r = 0; r < W; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s_qf + w0 + r);
+          y[r] *= f.x, y[r + 1] *= f.y, y[r + 2] *= f.z, y[r + 3] *= f.w;
+        }
 #pragma unroll
       for (int r = 0; r < W; r += 4) {
         const float4 m = *reinterpret_cast<const float4*>(s_neg + w0 + r);
-        const float4 f = *reinterpret_cast<const float4*>(s_qf + w0 + r);
-        const uint64_t y0 = k8_mul2(k8_pair(y[r], y[r + 1]), k8_pair(f.x, f.y)),
-                       y1 = k8_mul2(k8_pair(y[r + 2], y[r + 3]), k8_pair(f.z, f.w));
-        k8_unpair(k8_fma2(y0, ct2, k8_add2(et2, k8_pair(m.x, m.y))), y[r], y[r + 1]);
-        k8_unpair(k8_fma2(y1, ct2, k8_add2(et2, k8_pair(m.z, m.w))), y[r + 2], y[r + 3]);
+        k8_unpair(k8_fma2(k8_pair(y[r], y[r + 1]), ct2, k8_add2(et2, k8_pair(m.x, m.y))), y[r], y[r + 1]);
+        k8_unpair(k8_fma2(k8_pair(y[r + 2], y[r + 3]), ct2, k8_add2(et2, k8_pair(m.z, m.w))), y[r + 2], y[r + 3]);
       }
       if (masked)
 #pragma unroll
@@ -1079,7 +1089,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   a.window = window;
   // exact for a group number below 2^26 and at most 64 groups to a page
   a.per_page = ((1ull << 32) + page_tokens / 16 - 1) / (page_tokens / 16);
-  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  a.scale_log2 = (float)(scale * (1.4426950408889634 / K8_QSCALE));
   // the narrowest tile that holds a sequence's rows, or the widest
   const long long wanted = (long long)a.max_rows * a.group;
   const int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : wanted <= 64 ? 64 : 128;

@@ -284,6 +284,27 @@ def test_a_row_alone_equals_the_row_in_its_chunk(dfl, cluster):
         np.testing.assert_array_equal(l1, lse[[j, 70 + j]])
 
 
+@pytest.mark.parametrize("cluster", [1, 4])
+def test_a_row_of_sharp_scores_leaves_its_neighbours_alone(dfl, cluster):
+    # some rows' scores jump by far more than 2^14 over their first chunk's: those come out right, and the
+    # other rows of their tile keep their bits
+    c = R.Case([(24, 1400)], 1, 128, 16, seed=19, q_heads=4)
+    cache = R.Cache(c)
+    k, v = 0.3 * c.vectors(1424), c.vectors(1424)
+    k[900, 0, 0], k[1300, 0, 0], k[200, 0, 1] = 40.0, 60.0, 50.0
+    cache.put_many(0, 0, k, v)
+    q = c.g.standard_normal((24, 4, 128))
+    q[:, :, :2] = 0.0
+    calm, calm_lse, _ = attend(dfl, c, cache, q, cluster_ctas=cluster)
+    q[5, 1, 0], q[11, 2, 0], q[17, 0, 1] = 30.0, 9.0, 20.0
+    got, lse, x = attend(dfl, c, cache, q, cluster_ctas=cluster)
+    compare(c, cache, got, lse, x)
+    same = np.ones((24, 4), bool)
+    same[5, 1] = same[11, 2] = same[17, 0] = False
+    np.testing.assert_array_equal(got[same], calm[same])
+    np.testing.assert_array_equal(lse[same], calm_lse[same])
+
+
 def test_joining_two_parts_by_lse(dfl):
     # attention over all keys = the parts' outputs weighted by their lse
     c = R.Case([(8, 500)], 1, 128, 16, seed=17, q_heads=4)
