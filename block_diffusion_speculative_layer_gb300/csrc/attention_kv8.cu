@@ -436,20 +436,51 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
 
   const Kv8Geom& g = a.g;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  constexpr int ISSUER = CT / 32, KEYS = ISSUER + 1, VALUES = ISSUER + 2;  // and the exponents' warp
+
+  // Barriers and tensor memory first: an earlier kernel may still run, and
+  // nothing that it writes is read before the wait.
+  pdl_trigger();
+  if (warp == ISSUER) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(k8_addr(&s_tmem)),
+                 "n"(L::COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    k8_fence_before();
+  }
+  if (warp == KEYS && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+    s_scaled = 0;
+    for (int i = 0; i < STAGES; ++i) {
+      k8_bar_init(bars + L::FK + i * 8, 1);
+      k8_bar_init(bars + L::FV + i * 8, 2);
+      k8_bar_init(bars + L::EK + i * 8, 1);
+      k8_bar_init(bars + L::EV + i * 8, CT / 32);
+    }
+    k8_bar_init(bars + L::SS, 1);        // S computed
+    k8_bar_init(bars + L::SR, CT / 32);  // S read, one arrival per softmax warp
+    k8_bar_init(bars + L::PW, CT / 32);  // V^T and P written
+    k8_bar_init(bars + L::OU, 1);        // O updated
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
   const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
   const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
   const int G = a.group;
-  constexpr int ISSUER = CT / 32, KEYS = ISSUER + 1, VALUES = ISSUER + 2;  // and exponents
 
   // The tile's rows; every CTA of a cluster takes the same way out.
   Kv8Seq sq;
   const bool fine = kv8_seq(g, s, sq) && sq.n <= a.max_rows;
-  if (!fine) {
-    if (threadIdx.x == 0) flag_error(g.err, ERR_BOUNDS);
+  const int r0 = tile * N, nr = fine ? min(N, sq.n * G - r0) : 0;
+  if (nr <= 0) {
+    if (!fine && threadIdx.x == 0) flag_error(g.err, ERR_BOUNDS);
+    __syncthreads();
+    k8_fence_after();
+    if (warp == ISSUER)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "n"(L::COLS) : "memory");
     return;
   }
-  const int r0 = tile * N, nr = min(N, sq.n * G - r0);
-  if (nr <= 0) return;
   const int len = sq.pos0 + sq.n;
 
   // Positions the rows see: they are in position order, so the first and the
@@ -537,21 +568,6 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   uint4 qw[QPASS];
 
   if (warp > ISSUER) {
-    if (warp == KEYS && lane == 0) {
-      s_scaled = 0;
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
-      for (int i = 0; i < STAGES; ++i) {
-        k8_bar_init(bars + L::FK + i * 8, 1);
-        k8_bar_init(bars + L::FV + i * 8, 2);
-        k8_bar_init(bars + L::EK + i * 8, 1);
-        k8_bar_init(bars + L::EV + i * 8, CT / 32);
-      }
-      k8_bar_init(bars + L::SS, 1);        // S computed
-      k8_bar_init(bars + L::SR, CT / 32);  // S read, one arrival per softmax warp
-      k8_bar_init(bars + L::PW, CT / 32);  // V^T and P written
-      k8_bar_init(bars + L::OU, 1);        // O updated
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
     // the first stages start before the other warps are ready
     Place p[STAGES];
 #pragma unroll
@@ -561,13 +577,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
 #pragma unroll
     for (unsigned i = 0; i < STAGES; ++i)
       if (i < n_mine) produce(i, checked(p[i]), one);
-  } else if (warp == ISSUER) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(k8_addr(&s_tmem)),
-                 "n"(L::COLS)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    k8_fence_before();
-  } else {
+  } else if (warp < ISSUER) {
 #pragma unroll
     for (int i = 0; i < QPASS; ++i) {
       const int r = threadIdx.x / LPR + i * RPP;
@@ -1034,19 +1044,8 @@ static cudaError_t k8_launch(const Kv8Attn& a, const CUtensorMap& map, int clust
     if ((e = k8_attrs<HD, N>()) != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)((long long)cluster * a.g.nseq * a.tiles), a.g.heads, 1);
-  c.blockDim = dim3(K8<HD, N>::THREADS);
-  c.dynamicSmemBytes = K8<HD, N>::BYTES;
-  c.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  c.attrs = at;
-  c.numAttrs = cluster > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kv8_attention_kernel<HD, N>, a, map);
+  return launch_kcl(kv8_attention_kernel<HD, N>, dim3((unsigned)((long long)cluster * a.g.nseq * a.tiles), a.g.heads, 1),
+                    dim3(K8<HD, N>::THREADS), (size_t)K8<HD, N>::BYTES, st, dim3(cluster, 1, 1), a, map);
 }
 
 }  // namespace dfk
@@ -1096,12 +1095,17 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   const long long tiles = (wanted + n - 1) / n;
   if (tiles * nseq > 0x7fffffff / 16) return DF_EINVAL;
   a.tiles = (int)tiles;
-  // enough CTAs for two on every SM, but two chunks at least for each
+  // The most CTAs to a tile that all run at once and have a chunk each.  (A
+  // second wave costs more than a longer first one: 4 x 8192 with 40 heads, 32
+  // tiles, 37 us with 4 CTAs to a tile and 71 us with 8; 16 blocks at 16384,
+  // 128 tiles, 120 us with 2 and 128 us with 4; one block at 1024, 8 tiles and
+  // 9 chunks, 20 us with 1 and 12.8 us with 8.)
   int cluster = cluster_ctas;
   if (!cluster) {
     const long long chunks = ((long long)max_len + K8_CHUNK - 1) / K8_CHUNK, work = tiles * nseq * n_kv_heads;
+    const long long room = (long long)K8_SMS * (n == 128 ? K8<128, 128>::PER_SM : K8<128, 64>::PER_SM);
     cluster = 1;
-    while (cluster < 16 && work * cluster < 2 * K8_SMS && chunks >= 4 * cluster) cluster *= 2;
+    while (cluster < 16 && 2 * work * cluster <= room && 2 * cluster <= chunks) cluster *= 2;
   }
   CUtensorMap map;
   if (!k8_tmap(&map, a.g)) return DF_ECUDA;

@@ -3,13 +3,14 @@
 
 namespace dfk {
 
-// Eight consecutive elements of a row.
+// Eight consecutive elements of a row.  (Plain loads, here and below: the
+// kernel may have started before the one that writes the rows had finished.)
 __device__ __forceinline__ void kv8_load8(const float* p, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 __device__ __forceinline__ void kv8_load8(const __nv_bfloat16* p, float* x) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -38,13 +39,15 @@ __device__ __forceinline__ void kv8_store8(__nv_bfloat16* p, const float* x) {
 // bytes are not this call's).
 constexpr int KV8_THREADS = 128;
 template <typename T, int HD>
-__global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Geom g, const T* __restrict__ k,
-                                                                const T* __restrict__ v, long long ks, long long vs) {
+__global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Geom g, const T* k,
+                                                                const T* v, long long ks, long long vs) {
   constexpr int LPV = HD / 8;                    // lanes per vector
   constexpr int VPP = KV8_THREADS / LPV;         // vectors per pass
   constexpr int PASSES = 2 * KV8_GROUP / VPP;
   __shared__ __align__(16) uint8_t sV[KV8_GROUP][HD];
   __shared__ uint8_t sE[KV8_GROUP][2];
+  pdl_trigger();
+  pdl_wait();
   const int s = kv8_unit_seq(g, blockIdx.x), head = blockIdx.y;
   if (s < 0) return;
   Kv8Seq q;
@@ -127,11 +130,13 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Geom g, const
 // Read: the same units, the other way.  The value plane is transposed through
 // shared memory, so both outputs leave in rows.
 template <typename T, int HD>
-__global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Geom g, T* __restrict__ k, T* __restrict__ v) {
+__global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Geom g, T* k, T* v) {
   constexpr int LPV = HD / 8;
   constexpr int VPP = KV8_THREADS / LPV;
   constexpr int PASSES = 2 * KV8_GROUP / VPP;
   __shared__ __align__(16) uint8_t sV[KV8_GROUP][HD];
+  pdl_trigger();
+  pdl_wait();
   const int s = kv8_unit_seq(g, blockIdx.x), head = blockIdx.y;
   if (s < 0) return;
   Kv8Seq q;
@@ -193,21 +198,13 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_read_kernel(Kv8Geom g, T* __r
 template <typename T>
 static cudaError_t launch_kv8_write(const Kv8Geom& g, const void* k, const void* v, long long ks, long long vs,
                                     cudaStream_t st) {
-  const dim3 grid(kv8_units(g.rows, g.nseq), g.heads);
-  if (g.hd == 128)
-    kv8_write_kernel<T, 128><<<grid, KV8_THREADS, 0, st>>>(g, (const T*)k, (const T*)v, ks, vs);
-  else
-    kv8_write_kernel<T, 64><<<grid, KV8_THREADS, 0, st>>>(g, (const T*)k, (const T*)v, ks, vs);
-  return cudaGetLastError();
+  return launch_k(g.hd == 128 ? kv8_write_kernel<T, 128> : kv8_write_kernel<T, 64>,
+                  dim3(kv8_units(g.rows, g.nseq), g.heads), dim3(KV8_THREADS), 0, st, g, (const T*)k, (const T*)v, ks, vs);
 }
 template <typename T>
 static cudaError_t launch_kv8_read(const Kv8Geom& g, void* k, void* v, cudaStream_t st) {
-  const dim3 grid(kv8_units(g.rows, g.nseq), g.heads);
-  if (g.hd == 128)
-    kv8_read_kernel<T, 128><<<grid, KV8_THREADS, 0, st>>>(g, (T*)k, (T*)v);
-  else
-    kv8_read_kernel<T, 64><<<grid, KV8_THREADS, 0, st>>>(g, (T*)k, (T*)v);
-  return cudaGetLastError();
+  return launch_k(g.hd == 128 ? kv8_read_kernel<T, 128> : kv8_read_kernel<T, 64>,
+                  dim3(kv8_units(g.rows, g.nseq), g.heads), dim3(KV8_THREADS), 0, st, g, (T*)k, (T*)v);
 }
 
 }  // namespace dfk
