@@ -59,13 +59,6 @@ __device__ __forceinline__ int kv8_unit_seq(const Kv8Geom& g, int unit) {
   return before - 1;
 }
 
-// The page of position `pos` of sequence s, or -1 (and the error bit).
-__device__ __forceinline__ int kv8_page(const Kv8Geom& g, int s, int pos) {
-  const int page = g.page_table[(size_t)s * g.pt_stride + pos / g.page_tokens];
-  if (page >= 0 && page < g.n_pages) return page;
-  flag_error(g.err, ERR_BOUNDS);
-  return -1;
-}
 __device__ __forceinline__ size_t kv8_code_at(const Kv8Geom& g, int page, int kv, int head) {
   return ((size_t)(page * 2 + kv) * g.heads + head) * g.page_tokens * g.hd;
 }
