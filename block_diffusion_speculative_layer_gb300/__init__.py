@@ -612,14 +612,24 @@ _kv8_env = None  # what the calls below look up once: their time is part of a sm
 
 
 def _kv8_bind():
-    """(uint8, int32, bf16, fp32, raw current stream of a device, current device, the three entry points)."""
+    """(uint8, int32, bf16, fp32, raw current stream of a device, current device, the three calls)."""
     global _kv8_env
     if _kv8_env is None:
+        import importlib.machinery
+        import importlib.util
         import torch
         torch.cuda.init()
         L = lib()
+        path = os.path.join(_HERE, "_lib", "kv8_call.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"kv8_call.so is missing ({path}); build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("kv8_call", path)
+        call = importlib.util.module_from_spec(importlib.util.spec_from_loader("kv8_call", loader))
+        loader.exec_module(call)
+        call.bind(*(ctypes.cast(f, _P).value for f in (L.df_op_kv8_write, L.df_op_kv8_read, L.df_op_attention_kv8)))
         _kv8_env = (torch.uint8, torch.int32, torch.bfloat16, torch.float32, torch._C._cuda_getCurrentRawStream,
-                    torch._C._cuda_getDevice, L.df_op_kv8_write, L.df_op_kv8_read, L.df_op_attention_kv8)
+                    torch._C._cuda_getDevice, call.write, call.read, call.attention)
     return _kv8_env
 
 
@@ -652,22 +662,17 @@ def _kv8_plan(cache: KV8Cache, page_table, row_start, kv_len, u8, i32):
     return dev, shape, nseq, table[1]
 
 
-def _kv8_call(dev: int, stream, current: int, raw_stream, what: str, fn, *args):
-    """fn(*args, stream) on device `dev`'s current stream, or on `stream`."""
-    if stream is None:
-        handle = raw_stream(dev)
-    elif stream.device_index != dev:
+def _kv8_stream(stream, dev: int) -> int:
+    if stream.device_index != dev:
         _kv8_refuse("the stream belongs to another device")
-    else:
-        handle = stream.cuda_stream
-    if current == dev:
-        st = fn(*args, handle)
-    else:
-        import torch
-        with torch.cuda.device(dev):
-            st = fn(*args, handle)
-    if st != DF_OK:
-        raise DfError(st, what)
+    return stream.cuda_stream
+
+
+def _kv8_elsewhere(dev: int, fn, args) -> int:
+    """fn(*args) with `dev` as the current device."""
+    import torch
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _kv8_empty(shape, dtype, dev: int, stream):
@@ -701,9 +706,12 @@ def kv8_write(cache: KV8Cache, k, v, page_table, row_start, kv_len, stream=None)
         _kv8_refuse("the heads of a row must be contiguous")
     if rows < 2:  # a single row's stride says nothing
         ks = vs = heads * hd
-    _kv8_call(dev, stream, current(), raw, "df_op_kv8_write", fn, k.data_ptr(), v.data_ptr(), dt, rows, ks, vs,
-              cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(), entries,
-              row_start.data_ptr(), kv_len.data_ptr(), nseq, cache.err.data_ptr())
+    args = (k.data_ptr(), v.data_ptr(), dt, rows, ks, vs, cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads,
+            hd, page_table.data_ptr(), entries, row_start.data_ptr(), kv_len.data_ptr(), nseq, cache.err.data_ptr(),
+            raw(dev) if stream is None else _kv8_stream(stream, dev))
+    st = fn(*args) if current() == dev else _kv8_elsewhere(dev, fn, args)
+    if st != DF_OK:
+        raise DfError(st, "df_op_kv8_write")
 
 
 def kv8_read(cache: KV8Cache, page_table, row_start, kv_len, rows: int, dtype=None, k=None, v=None, stream=None):
@@ -726,9 +734,12 @@ def kv8_read(cache: KV8Cache, page_table, row_start, kv_len, rows: int, dtype=No
         v = _kv8_empty(shape, dtype, dev, stream)
     elif v.get_device() != dev or v.dtype is not dtype or v.shape != shape or not v.is_contiguous():
         _kv8_refuse("v must be a contiguous [rows, heads, head_dim] tensor of the type")
-    _kv8_call(dev, stream, current(), raw, "df_op_kv8_read", fn, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
-              page, heads, hd, page_table.data_ptr(), entries, row_start.data_ptr(), kv_len.data_ptr(), nseq, rows,
-              dt, k.data_ptr(), v.data_ptr(), cache.err.data_ptr())
+    args = (cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(), entries,
+            row_start.data_ptr(), kv_len.data_ptr(), nseq, rows, dt, k.data_ptr(), v.data_ptr(), cache.err.data_ptr(),
+            raw(dev) if stream is None else _kv8_stream(stream, dev))
+    st = fn(*args) if current() == dev else _kv8_elsewhere(dev, fn, args)
+    if st != DF_OK:
+        raise DfError(st, "df_op_kv8_read")
     return k, v
 
 
@@ -771,9 +782,11 @@ def attention_kv8(q, cache: KV8Cache, page_table, row_start, kv_len, max_rows: i
         max_rows = rows
     if max_len > _I32_MAX or window > _I32_MAX:
         max_len, window = min(max_len, _I32_MAX), min(window, _I32_MAX)
-    _kv8_call(dev, stream, current(), raw, "df_op_attention_kv8", fn, q.data_ptr(), qs, out.data_ptr(), os_, lse_ptr,
-              rows, hq, cache.codes.data_ptr(), cache.exps.data_ptr(), n, page, heads, hd, page_table.data_ptr(),
-              entries, row_start.data_ptr(), kv_len.data_ptr(), nseq, int(max_rows), int(max_len),
-              scale if scale is not None else hd ** -0.5, 1 if causal else 0, int(window), cluster_ctas,
-              cache.err.data_ptr())
+    args = (q.data_ptr(), qs, out.data_ptr(), os_, lse_ptr, rows, hq, cache.codes.data_ptr(), cache.exps.data_ptr(), n,
+            page, heads, hd, page_table.data_ptr(), entries, row_start.data_ptr(), kv_len.data_ptr(), nseq, max_rows,
+            max_len, hd ** -0.5 if scale is None else scale, 1 if causal else 0, window, cluster_ctas,
+            cache.err.data_ptr(), raw(dev) if stream is None else _kv8_stream(stream, dev))
+    st = fn(*args) if current() == dev else _kv8_elsewhere(dev, fn, args)
+    if st != DF_OK:
+        raise DfError(st, "df_op_attention_kv8")
     return out, lse

@@ -1,8 +1,10 @@
 """Build the engine's shared library (libdflash.so) for sm_103a with nvcc.
 
 Each .cu file under csrc/ compiles to an object in parallel; the objects link
-into ``_lib/libdflash.so`` next to this file (in-tree, git-ignored).  A build
-is skipped when the library is newer than every source and header.
+into ``_lib/libdflash.so`` next to this file (in-tree, git-ignored), and
+csrc/kv8_call.cpp, the CPython form of the 8-bit cache calls, compiles to
+``_lib/kv8_call.so``.  A build is skipped when both are newer than every source
+and header.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libdflash.so")
+CALL_SRC = os.path.join(CSRC, "kv8_call.cpp")
+CALL = os.path.join(OUT_DIR, "kv8_call.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]
@@ -36,10 +41,10 @@ def _sources():
 
 
 def _up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALL):
         return False
-    t = os.path.getmtime(LIB)
-    deps = _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
+    deps = _sources() + [CALL_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     return all(os.path.getmtime(p) <= t for p in deps)
 
@@ -64,8 +69,18 @@ def build(verbose: bool = False, force: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
+    def compile_call():
+        cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+               "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], CALL_SRC, "-o", CALL + ".tmp"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"compiling kv8_call.cpp failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(CALL + ".tmp", CALL)
+
     with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+        call = pool.submit(compile_call)
         objs = list(pool.map(compile_one, _sources()))
+        call.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
