@@ -438,6 +438,10 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int ISSUER = CT / 32, KEYS = ISSUER + 1, VALUES = ISSUER + 2;  // and the exponents' warp
 
+  const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
+  const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
+  const int G = a.group;
+
   // Barriers and tensor memory first: an earlier kernel may still run, and
   // nothing that it writes is read before the wait.
   pdl_trigger();
@@ -465,9 +469,20 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   }
   pdl_wait();
 
-  const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
-  const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
-  const int G = a.group;
+  // Pages of the first stages, looked up while the sequence's entries are on
+  // their way: without a window chunk c of rank r starts at r + c C whatever
+  // the lengths are.
+  int early[STAGES];
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) {
+    early[i] = -1;
+    if (warp > ISSUER && lane < 8 && a.window == 0) {
+      const unsigned entry =
+          (unsigned)(((unsigned long long)((unsigned)(rank + i * C) * (K8_CHUNK / 16) + lane) * a.per_page) >> 32);
+      if (entry < (unsigned)g.pt_stride) early[i] = g.page_table[(size_t)s * g.pt_stride + entry];
+    }
+  }
+
 
   // The tile's rows; every CTA of a cluster takes the same way out.
   Kv8Seq sq;
@@ -488,7 +503,12 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   // sequence belongs to rank c % C.
   auto lowest = [&](int pos) { return a.window > 0 ? max(0, pos - a.window + 1) : 0; };
   auto highest = [&](int pos) { return pos < 0 ? -1 : a.causal ? pos : len - 1; };
-  const int pos_first = sq.pos0 + r0 / G, pos_last = sq.pos0 + (r0 + nr - 1) / G;
+  // row r of the tile: head (g0 + r) % G of the group, of token j0 + (g0 + r) / G
+  // (the quotient of small numbers by a reciprocal: off by less than half a step)
+  const int j0 = r0 / G, g0 = r0 - j0 * G;
+  const float inv_g = 1.f / (float)G;
+  auto token = [&](int r) { return j0 + (int)(((float)(g0 + r) + 0.5f) * inv_g); };
+  const int pos_first = sq.pos0 + j0, pos_last = sq.pos0 + token(nr - 1);
   const int full_lo = lowest(pos_last), full_hi = highest(pos_first), end = highest(pos_last) + 1;
   const int c_end = (end + K8_CHUNK - 1) / K8_CHUNK;
   int c_first = min(lowest(pos_first), len) / K8_CHUNK;
@@ -502,13 +522,14 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   struct Place {
     int page, slot;  // page -2: no such group
   };
-  auto place = [&](unsigned i) {
+  auto place = [&](unsigned i, int known = 0x7fffffff) {
     Place p{-2, 0};
     if (i < n_mine && lane < 8) {
       const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + lane;
       const unsigned entry = (unsigned)(((unsigned long long)group * a.per_page) >> 32);  // group / groups of a page
       p.slot = (int)(group * 16 - entry * g.page_tokens);
-      if ((int)group * 16 < len) p.page = g.page_table[(size_t)s * g.pt_stride + entry];
+      if ((int)group * 16 < len)
+        p.page = known != 0x7fffffff ? known : g.page_table[(size_t)s * g.pt_stride + entry];
     }
     return p;
   };
@@ -568,22 +589,15 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   uint4 qw[QPASS];
 
   if (warp > ISSUER) {
-    // the first stages start before the other warps are ready
-    Place p[STAGES];
-#pragma unroll
-    for (unsigned i = 0; i < STAGES; ++i) p[i] = place(i);
-    const uint32_t one = k8_elect();
-    asm volatile("bar.sync 11, 96;" ::: "memory");
-#pragma unroll
-    for (unsigned i = 0; i < STAGES; ++i)
-      if (i < n_mine) produce(i, checked(p[i]), one);
+    // (nothing that the others wait for, but that they are here)
+    asm volatile("bar.arrive 12, %0;" ::"n"(L::THREADS) : "memory");
   } else if (warp < ISSUER) {
 #pragma unroll
     for (int i = 0; i < QPASS; ++i) {
       const int r = threadIdx.x / LPR + i * RPP;
       qw[i] = make_uint4(0, 0, 0, 0);
       if (r < nr) {
-        const int j = (r0 + r) / G, h = head * G + (r0 + r) - j * G;
+        const int j = token(r), h = head * G + (r0 + r) - j * G;
         if (sq.pos0 + j >= 0)
           qw[i] = *reinterpret_cast<const uint4*>(a.q + (sq.row0 + j) * a.qs + (size_t)h * HD + sub * 8);
         if (sub == 0) {
@@ -602,10 +616,9 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       }
     }
   }
-  __syncthreads();
+  if (warp <= ISSUER) asm volatile("bar.sync 12, %0;" ::"n"(L::THREADS) : "memory");
   k8_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-
+  const uint32_t tmem = warp <= ISSUER ? __shfl_sync(0xffffffffu, s_tmem, 0) : 0;
   if (warp >= ISSUER)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::AREGS));
   else
@@ -613,6 +626,10 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
 
   if (warp > ISSUER) {
     const uint32_t one = k8_elect();
+    asm volatile("bar.sync 11, 96;" ::: "memory");  // the barriers are initialised
+#pragma unroll
+    for (unsigned i = 0; i < STAGES; ++i)
+      if (i < n_mine) produce(i, checked(a.window == 0 ? place(i, early[i]) : place(i)), one);
     Place next = place(STAGES);
     for (unsigned i = STAGES; i < n_mine; ++i) {
       const Place p = checked(next);
@@ -904,27 +921,21 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
               sum == 0.f ? -INFINITY : (s_m[r] == -INFINITY ? sum : 0.6931471805599453f * (s_m[r] - K8_BIAS) + logf(sum));
       }
       k8_group_sync(group);
-#pragma unroll 1
-      for (int cc = w0; cc < w0 + W && cc < nr; cc += 8) {
-        float o[8];
-        k8_ld<8>(lane_base + L::OCOL + cc, o);  // anything if no product was made: not used then
+      float o[W];
+      k8_ld<W>(lane_base + L::OCOL + w0, o);  // anything if no product was made: not used then
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          if (cc + r >= nr || t >= HD) continue;
-          const float v = s_l[cc + r] == 0.f ? 0.f : o[r] * s_fac[cc + r];
-          a.out[s_tok[cc + r] * a.os + s_hd[cc + r] * HD + t] = __float2bfloat16_rn(v);
-        }
+      for (int r = 0; r < W; ++r) {
+        if (w0 + r >= nr || t >= HD) break;
+        const float v = s_l[w0 + r] == 0.f ? 0.f : o[r] * s_fac[w0 + r];
+        a.out[s_tok[w0 + r] * a.os + s_hd[w0 + r] * HD + t] = __float2bfloat16_rn(v);
       }
     } else if (n_mine > 0) {
       float* part = reinterpret_cast<float*>(sm);
-#pragma unroll 1
-      for (int cc = w0; cc < w0 + W && cc < nr; cc += 8) {
-        float o[8];
-        k8_ld<8>(lane_base + L::OCOL + cc, o);
-        if (t < HD)
+      float o[W];
+      k8_ld<W>(lane_base + L::OCOL + w0, o);
+      if (t < HD)
 #pragma unroll
-          for (int r = 0; r < 8; ++r) part[(cc + r) * L::OLD + t] = o[r];
-      }
+        for (int r = 0; r < W; ++r) part[(w0 + r) * L::OLD + t] = o[r];
     }
   }
   k8_fence_before();
@@ -935,57 +946,53 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   }
   if (C == 1) return;
 
-  // ---- merge: rank q finishes rows q, q + C, ...: first the parts' weights,
-  // then HD / 4 threads to a row
+  // ---- merge: rank q finishes rows q, q + C, ..., HD / 4 lanes to a row, lane
+  // i of them reading rank i's maximum and sum beside everyone's part
   k8_cluster_sync();
-  __shared__ float s_w[16][(N + 1) / 2], s_sum[(N + 1) / 2], s_top[(N + 1) / 2];
-  const int mine = nr > rank ? (nr - rank + C - 1) / C : 0;
   if (warp < ISSUER) {
-    for (int r = threadIdx.x >> 4; r < mine; r += CT / 16) {  // 16 lanes to a row, one per rank
-      const int row = rank + C * r, q = lane & 15;
+    constexpr int TPR = HD / 4;
+    const uint32_t lanes = TPR == 32 ? 0xffffffffu : 0xffffu << (lane & 16);
+    const int sub4 = lane % TPR, d = sub4 * 4;
+    for (int row = rank + C * (threadIdx.x / TPR); row < nr; row += C * (CT / TPR)) {
+      const uint32_t part = smb + (row * L::OLD + d) * 4;
       float m = -INFINITY, lq = 0.f;
-      if (q < C) {
-        m = k8_remote_f(k8_remote(k8_addr(s_m) + row * 4, q));
-        lq = k8_remote_f(k8_remote(k8_addr(s_l) + row * 4, q));
+      if (sub4 < C) {
+        m = k8_remote_f(k8_remote(k8_addr(s_m) + row * 4, sub4));
+        lq = k8_remote_f(k8_remote(k8_addr(s_l) + row * 4, sub4));
       }
-      const uint32_t half = 0xffffu << (lane & 16);
+      float4 x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)  // (a rank without a chunk left no part: its weight is 0, its bytes are not used)
+        if (q < C) x[q] = k8_remote_f4(k8_remote(part, q));
       float M = m;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(half, M, o));
+      for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, o));
       const float w = lq == 0.f ? 0.f : k8_ex2(m - M);  // 0: no key of this row there
       float sum = lq * w;
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
-      s_w[q][r] = w;
-      if (q == 0) {
-        s_sum[r] = sum;
-        s_top[r] = M;
-      }
-    }
-    k8_all_sync<CT>();
-    constexpr int TPR = HD / 4;
-    const int d = (threadIdx.x % TPR) * 4;
-    for (int r = threadIdx.x / TPR; r < mine; r += CT / TPR) {
-      const int row = rank + C * r;
-      const uint32_t part = smb + (row * L::OLD + d) * 4;
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+      M = __shfl_sync(lanes, M, 0, TPR);
+      sum = __shfl_sync(lanes, sum, 0, TPR);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q0 = 0; q0 < C; q0 += 4) {
-        float4 x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (q0 + e < C && s_w[q0 + e][r] != 0.f) x[e] = k8_remote_f4(k8_remote(part, q0 + e));
+      auto add = [&](const float4& p, int q) {
+        const float wq = __shfl_sync(lanes, w, q, TPR);
+        if (wq != 0.f) {
+          o.x = fmaf(p.x, wq, o.x);
+          o.y = fmaf(p.y, wq, o.y);
+          o.z = fmaf(p.z, wq, o.z);
+          o.w = fmaf(p.w, wq, o.w);
         }
+      };
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = q0 + e < C ? s_w[q0 + e][r] : 0.f;
-          o.x = fmaf(x[e].x, w, o.x);
-          o.y = fmaf(x[e].y, w, o.y);
-          o.z = fmaf(x[e].z, w, o.z);
-          o.w = fmaf(x[e].w, w, o.w);
-        }
+      for (int q = 0; q < 8; ++q)
+        if (q < C) add(x[q], q);
+      if (C > 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = k8_remote_f4(k8_remote(part, 8 + q));
+#pragma unroll
+        for (int q = 0; q < 8; ++q) add(x[q], 8 + q);
       }
-      const float sum = s_sum[r], M = s_top[r], inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long at = s_tok[row];
       const int hq = s_hd[row];
       const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv),
