@@ -13,11 +13,11 @@
 // scale log2 e, and e_t = b_v - 127 added to the exponent).
 //
 // Keys go from the cache's bytes to the tensor core without a conversion: a
-// bf16 query has 8 bits, so 32 q is the sum of two e4m3 numbers of 4 bits each,
-// exactly down to |q| = 2^-7 and to within 2^-15 below.  A row whose largest
-// magnitude is outside [1/4, 8) is first brought to [4, 8) by a power of two
-// f_r, and the scores of its tile are multiplied by f_r.  Both products go to
-// one accumulator.
+// bf16 query has 8 bits, so 64 q is the sum of two e4m3 numbers of 4 bits each,
+// exactly down to |q| = 2^-8 and to within 2^-16 below.  A row whose largest
+// magnitude is outside [1/4, 7] is first brought to (3.5, 7] by a power of two
+// f_r, and the scores of its tile are multiplied by f_r (5% of a long chunk's
+// time, so not for every tile).  Both products go to one accumulator.
 // Values need P at more than 8 bits and a wide range, so their product is f16:
 // a thread widens its head dim's codes of 128 values (the cache keeps values
 // transposed), exactly, and stores them to its own lane of tensor memory, the
@@ -72,7 +72,7 @@ constexpr int K8_CHUNK = 128;     // keys per chunk: one per tensor-memory lane
 constexpr int K8_SMS = 152;
 constexpr float K8_SLACK = 8.f;   // how far (log2) a term may pass M before M moves
 constexpr float K8_BIAS = 6.f;    // P = 2^K8_BIAS for a term at M
-constexpr float K8_QSCALE = 32.f; // queries are staged times this
+constexpr float K8_QSCALE = 64.f; // queries are staged times this (7 * 64 = 448, the largest e4m3 number)
 constexpr unsigned long long K8_WAIT_NS = 2000000000ull;
 
 // Shapes and shared memory of a CTA (offsets from a 1024-byte boundary).
@@ -700,7 +700,8 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       for (int o = LPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       // the power of two taken out of the row (a row that holds no numbers becomes NaN)
       const int e = (int)(top >> 7) - 127;
-      const int out = top == 0 || (e >= -2 && e < 3) ? 0 : min(max(e - 2, -114), 120);
+      const bool fits = top == 0 || (top >= 0x3E80u && top <= 0x40E0u);  // bf16 bits of 1/4 and 7
+      const int out = fits ? 0 : min(max(e - 2 + ((top & 0x7Fu) > 0x60u ? 1 : 0), -113), 120);
       const float by = top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : K8_QSCALE * kv8_pow2(-out);
       float x[8], hi[8];
 #pragma unroll
