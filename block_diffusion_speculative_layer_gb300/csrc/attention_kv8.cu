@@ -439,7 +439,8 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   constexpr int ISSUER = CT / 32, KEYS = ISSUER + 1, VALUES = ISSUER + 2;  // and the exponents' warp
 
   const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
-  const int head = blockIdx.y, s = (int)(blockIdx.x / C) / a.tiles, tile = (int)(blockIdx.x / C) % a.tiles;
+  const int lg = 31 - __clz(C);  // clusters are powers of two
+  const int head = blockIdx.y, s = (int)(blockIdx.x >> lg) / a.tiles, tile = (int)(blockIdx.x >> lg) - s * a.tiles;
   const int G = a.group;
 
   // Barriers and tensor memory first: an earlier kernel may still run, and
@@ -512,8 +513,8 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const int full_lo = lowest(pos_last), full_hi = highest(pos_first), end = highest(pos_last) + 1;
   const int c_end = (end + K8_CHUNK - 1) / K8_CHUNK;
   int c_first = min(lowest(pos_first), len) / K8_CHUNK;
-  c_first += (rank - c_first % C + C) % C;
-  const unsigned n_mine = c_end > c_first ? (c_end - c_first + C - 1) / C : 0;
+  c_first += (rank - c_first) & (C - 1);
+  const unsigned n_mine = c_end > c_first ? (unsigned)(c_end - c_first + C - 1) >> lg : 0;
 
   bool ok = true;
   // Staging: a chunk's 8 groups of 16 keys, of values and of exponents are 24
@@ -922,14 +923,24 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
               sum == 0.f ? -INFINITY : (s_m[r] == -INFINITY ? sum : 0.6931471805599453f * (s_m[r] - K8_BIAS) + logf(sum));
       }
       k8_group_sync(group);
+      // through shared memory (the tiles have been read): stores of 16 bytes
+      // instead of 2, 1118 rows of 19 sequences 153 us, 161 with the latter
       float o[W];
       k8_ld<W>(lane_base + L::OCOL + w0, o);  // anything if no product was made: not used then
+      __nv_bfloat16* rows = reinterpret_cast<__nv_bfloat16*>(sm) + w0 * HD;
+      if (t < HD)
 #pragma unroll
-      for (int r = 0; r < W; ++r) {
-        if (w0 + r >= nr || t >= HD) break;
-        const float v = s_l[w0 + r] == 0.f ? 0.f : o[r] * s_fac[w0 + r];
-        a.out[s_tok[w0 + r] * a.os + s_hd[w0 + r] * HD + t] = __float2bfloat16_rn(v);
-      }
+        for (int r = 0; r < W; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s_fac + w0 + r);
+          rows[r * HD + t] = __float2bfloat16_rn(f.x == 0.f ? 0.f : o[r] * f.x);
+          rows[(r + 1) * HD + t] = __float2bfloat16_rn(f.y == 0.f ? 0.f : o[r + 1] * f.y);
+          rows[(r + 2) * HD + t] = __float2bfloat16_rn(f.z == 0.f ? 0.f : o[r + 2] * f.z);
+          rows[(r + 3) * HD + t] = __float2bfloat16_rn(f.w == 0.f ? 0.f : o[r + 3] * f.w);
+        }
+      k8_group_sync(group);
+      for (int r = t / LPR; r < W && w0 + r < nr; r += 128 / LPR)
+        *reinterpret_cast<uint4*>(a.out + s_tok[w0 + r] * a.os + s_hd[w0 + r] * HD + t % LPR * 8) =
+            *reinterpret_cast<const uint4*>(rows + r * HD + t % LPR * 8);
     } else if (n_mine > 0) {
       float* part = reinterpret_cast<float*>(sm);
       float o[W];
@@ -1097,9 +1108,24 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   // exact for a group number below 2^26 and at most 64 groups to a page
   a.per_page = ((1ull << 32) + page_tokens / 16 - 1) / (page_tokens / 16);
   a.scale_log2 = (float)(scale * (1.4426950408889634 / K8_QSCALE));
-  // the narrowest tile that holds a sequence's rows, or the widest
+  // The narrowest tile that holds a sequence's rows.  More than 64 rows take
+  // tiles of 128, which read the cache half as often (8 chunks of 1737 rows, 95
+  // tiles each: 234 us, 283 with 64), unless twice as many tiles of 64 leave
+  // every CTA an SM of its own (100 rows of 4 sequences, 2 heads: 11.5 us, 12.9
+  // with 128).
   const long long wanted = (long long)a.max_rows * a.group;
-  const int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : wanted <= 64 ? 64 : 128;
+  auto clusters = [&](int n) {  // CTAs to a tile, see below
+    if (cluster_ctas) return (long long)cluster_ctas;
+    const long long span = window ? (long long)window + (n - 1) / a.group + 1 : max_len;
+    const long long chunks = ((span < max_len ? span : max_len) + K8_CHUNK - 1) / K8_CHUNK;
+    const long long work = (wanted + n - 1) / n * nseq * n_kv_heads;
+    const long long room = (long long)K8_SMS * (n == 128 ? K8<128, 128>::PER_SM : K8<128, 64>::PER_SM);
+    long long c = 1;
+    while (c < 16 && 2 * work * c <= room && 2 * c <= chunks) c *= 2;
+    return c;
+  };
+  int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : 64;
+  if (wanted > 64 && (wanted + 63) / 64 * nseq * n_kv_heads * clusters(64) > K8_SMS) n = 128;
   const long long tiles = (wanted + n - 1) / n;
   if (tiles * nseq > 0x7fffffff / 16) return DF_EINVAL;
   a.tiles = (int)tiles;
@@ -1107,14 +1133,10 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   // second wave costs more than a longer first one: 4 x 8192 with 40 heads, 32
   // tiles, 37 us with 4 CTAs to a tile and 71 us with 8; 16 blocks at 16384,
   // 128 tiles, 120 us with 2 and 128 us with 4; one block at 1024, 8 tiles and
-  // 9 chunks, 20 us with 1 and 12.8 us with 8.)
-  int cluster = cluster_ctas;
-  if (!cluster) {
-    const long long chunks = ((long long)max_len + K8_CHUNK - 1) / K8_CHUNK, work = tiles * nseq * n_kv_heads;
-    const long long room = (long long)K8_SMS * (n == 128 ? K8<128, 128>::PER_SM : K8<128, 64>::PER_SM);
-    cluster = 1;
-    while (cluster < 16 && 2 * work * cluster <= room && 2 * cluster <= chunks) cluster *= 2;
-  }
+  // 9 chunks, 20 us with 1 and 12.8 us with 8.
+  // A window's tile meets few chunks: 16 blocks of 19 rows at 8000 with a window
+  // of 1, 9.6 us instead of 16.4.)
+  const int cluster = (int)clusters(n);
   CUtensorMap map;
   if (!k8_tmap(&map, a.g)) return DF_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
