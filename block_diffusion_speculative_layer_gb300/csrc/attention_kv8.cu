@@ -51,6 +51,7 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "kv8.cuh"
@@ -64,6 +65,7 @@ struct Kv8Attn {
   float* lse;
   long long qs, os;  // row strides (elements)
   int q_heads, group, max_rows, causal, window, tiles;
+  unsigned solo;                // tiles that one CTA takes alone
   float scale_log2;
   unsigned long long per_page;  // 2^32 / (groups of 16 tokens of a page), rounded up
 };
@@ -438,9 +440,15 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int ISSUER = CT / 32, KEYS = ISSUER + 1, VALUES = ISSUER + 2;  // and the exponents' warp
 
-  const int C = (int)k8_cluster_size(), rank = (int)k8_rank();
+  // The first `solo` CTAs take a tile each, the clusters behind them share one.
+  // Of a causal sequence's tiles the last, which sees the most, starts first.
+  const bool alone = blockIdx.x < a.solo;
+  const int C = alone ? 1 : (int)k8_cluster_size(), rank = alone ? 0 : (int)k8_rank();
   const int lg = 31 - __clz(C);  // clusters are powers of two
-  const int head = blockIdx.y, s = (int)(blockIdx.x >> lg) / a.tiles, tile = (int)(blockIdx.x >> lg) - s * a.tiles;
+  const unsigned unit = alone ? blockIdx.x : a.solo + ((blockIdx.x - a.solo) >> lg);
+  const int head = (int)(unit / (unsigned)(a.tiles * g.nseq)), in_head = (int)unit - head * a.tiles * g.nseq;
+  const int s = in_head / a.tiles, nth = in_head - s * a.tiles;
+  const int tile = a.causal && a.window == 0 ? a.tiles - 1 - nth : nth;
   const int G = a.group;
 
   // Barriers and tensor memory first: an earlier kernel may still run, and
@@ -1063,8 +1071,33 @@ static cudaError_t k8_launch(const Kv8Attn& a, const CUtensorMap& map, int clust
     if ((e = k8_attrs<HD, N>()) != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
-  return launch_kcl(kv8_attention_kernel<HD, N>, dim3((unsigned)((long long)cluster * a.g.nseq * a.tiles), a.g.heads, 1),
+  return launch_kcl(kv8_attention_kernel<HD, N>, dim3(a.solo + ((unsigned)a.tiles * a.g.nseq * a.g.heads - a.solo) * cluster, 1, 1),
                     dim3(K8<HD, N>::THREADS), (size_t)K8<HD, N>::BYTES, st, dim3(cluster, 1, 1), a, map);
+}
+
+// Estimate (us) of a call in tiles of n rows, c CTAs to a tile, from times
+// measured with 8 to 256 tiles of 3 to 257 chunks: what a CTA takes for a chunk
+// and for the rest, what joining the parts adds, and what CTAs cost one another
+// (a second on an SM; with c = 1 from fewer).  More clusters than run at once
+// cost a second round (that depends on how the SMs are grouped: 16 tiles, 2048
+// positions, 16 rows: 15 us with 4 or 8 CTAs to a tile, 25 with 16).  Estimate
+// and time of 16 rows of 4 heads, c = 1, 4, 8: one sequence at 512, 8 tiles,
+// 12.1 11.1 10.1 and 12.1 10.9 10.0; two at 1024, 16.3 12.2 13.3 and 16.5 12.2
+// 14.1; four at 8192, 75 35 28 and 77 35 27.  Tiles of 64 and 128, c = 1: 32
+// rows of one sequence at 1024, 16.3 20.7 and 16.8 20.8; 64 rows of eight at
+// 8192, 111 94 and 108 98.
+static float k8_time(int n, int c, long long work, long long chunks) {
+  constexpr int fit[2][5] = {{304, 152, 74, 36, 14}, {152, 76, 36, 15, 7}};  // clusters at once
+  constexpr float chunk[4] = {0.66f, 0.8f, 1.05f, 1.3f}, rest[4] = {4.7f, 5.4f, 6.8f, 9.f},
+                  join[4] = {1.3f, 1.6f, 2.2f, 3.2f};
+  const int i = n == 16 ? 0 : n == 32 ? 1 : n == 64 ? 2 : 3;
+  const int j = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : c == 8 ? 3 : 4;
+  const long long ctas = work * c, rounds = (work + fit[i == 3][j] - 1) / fit[i == 3][j];
+  const bool shared = i < 3 && ctas > K8_SMS, busy = i < 3 && ctas > K8_SMS / 2;
+  const float slower = shared ? (c == 1 ? 1.5f : 1.8f) : busy ? 1.4f : i < 3 && c == 1 && ctas > K8_SMS / 4 ? 1.2f : 1.f;
+  const float fixed = rest[i] + (c == 1 ? 0.f : c == 2 || c == 16 ? 1.4f * join[i] : join[i]);
+  return (float)rounds *
+         (fixed * (shared ? 1.25f : busy ? 1.15f : 1.f) + (float)((chunks + c - 1) / c) * chunk[i] * slower);
 }
 
 }  // namespace dfk
@@ -1108,35 +1141,37 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   // exact for a group number below 2^26 and at most 64 groups to a page
   a.per_page = ((1ull << 32) + page_tokens / 16 - 1) / (page_tokens / 16);
   a.scale_log2 = (float)(scale * (1.4426950408889634 / K8_QSCALE));
-  // The narrowest tile that holds a sequence's rows.  More than 64 rows take
-  // tiles of 128, which read the cache half as often (8 chunks of 1737 rows, 95
-  // tiles each: 234 us, 283 with 64), unless twice as many tiles of 64 leave
-  // every CTA an SM of its own (100 rows of 4 sequences, 2 heads: 11.5 us, 12.9
-  // with 128).
+  // The narrowest tile that holds a sequence's rows; more than 64 rows are cut
+  // into tiles of 64 or 128.  A sequence's tiles are at most so many, and of
+  // all that many hold rows at most:
   const long long wanted = (long long)a.max_rows * a.group;
-  auto clusters = [&](int n) {  // CTAs to a tile, see below
-    if (cluster_ctas) return (long long)cluster_ctas;
+  auto all_of = [&](int n) { return (wanted + n - 1) / n * nseq * n_kv_heads; };
+  auto work_of = [&](int n) { return std::min(all_of(n), ((long long)rows * a.group / n + nseq) * n_kv_heads); };
+  auto chunks_of = [&](int n) {  // of the longest sequence, or of a tile's window
     const long long span = window ? (long long)window + (n - 1) / a.group + 1 : max_len;
-    const long long chunks = ((span < max_len ? span : max_len) + K8_CHUNK - 1) / K8_CHUNK;
-    const long long work = (wanted + n - 1) / n * nseq * n_kv_heads;
-    const long long room = (long long)K8_SMS * (n == 128 ? K8<128, 128>::PER_SM : K8<128, 64>::PER_SM);
-    long long c = 1;
-    while (c < 16 && 2 * work * c <= room && 2 * c <= chunks) c *= 2;
-    return c;
+    return (std::min<long long>(span, max_len) + K8_CHUNK - 1) / K8_CHUNK;
   };
-  int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : 64;
-  if (wanted > 64 && (wanted + 63) / 64 * nseq * n_kv_heads * clusters(64) > K8_SMS) n = 128;
+  int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : 64, cluster = 1;
+  float best = INFINITY;
+  for (int m = n; m <= (wanted > 64 ? 128 : n); m *= 2)
+    for (int c = cluster_ctas ? cluster_ctas : 1; c <= (cluster_ctas ? cluster_ctas : 16); c *= 2) {
+      if (!cluster_ctas && c / 2 >= std::max(chunks_of(m), 1ll)) break;
+      const float t = k8_time(m, c, work_of(m), chunks_of(m));
+      if (t < best) best = t, n = m, cluster = c;
+    }
   const long long tiles = (wanted + n - 1) / n;
-  if (tiles * nseq > 0x7fffffff / 16) return DF_EINVAL;
+  if (all_of(n) > 0x7fffffff / 16) return DF_EINVAL;
   a.tiles = (int)tiles;
-  // The most CTAs to a tile that all run at once and have a chunk each.  (A
-  // second wave costs more than a longer first one: 4 x 8192 with 40 heads, 32
-  // tiles, 37 us with 4 CTAs to a tile and 71 us with 8; 16 blocks at 16384,
-  // 128 tiles, 120 us with 2 and 128 us with 4; one block at 1024, 8 tiles and
-  // 9 chunks, 20 us with 1 and 12.8 us with 8.
-  // A window's tile meets few chunks: 16 blocks of 19 rows at 8000 with a window
-  // of 1, 9.6 us instead of 16.4.)
-  const int cluster = (int)clusters(n);
+  // Tiles that fill the GPU several times, and half of it or less at the end:
+  // those last ones are shared by two CTAs each (2048 rows at 6144, 512 tiles:
+  // 294 us, 315 without; 40 single rows at 8192, 320 tiles: 120 and 139; below
+  // 32 chunks there is nothing to gain: 48 blocks at 1024 43 and 39 us).
+  const long long room = (long long)K8_SMS * (n == 128 ? K8<128, 128>::PER_SM : K8<128, 64>::PER_SM);
+  if (!cluster_ctas && cluster == 1 && all_of(n) > room && all_of(n) == work_of(n) && chunks_of(n) >= 32 &&
+      all_of(n) % room && all_of(n) % room * 2 <= room) {
+    cluster = 2;
+    a.solo = (unsigned)(all_of(n) / room * room);
+  }
   CUtensorMap map;
   if (!k8_tmap(&map, a.g)) return DF_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
