@@ -3,21 +3,37 @@
 
 namespace dfk {
 
-// Eight consecutive elements of a row.  (Plain loads, here and below: the
-// kernel may have started before the one that writes the rows had finished.)
-__device__ __forceinline__ void kv8_load8(const float* p, float* x) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void kv8_load8(const __nv_bfloat16* p, float* x) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+// Eight consecutive elements of a row, as they lie and as floats.  (Plain
+// loads, here and below: the kernel may have started before the one that
+// writes the rows had finished.)
+template <typename T>
+struct Kv8Raw;
+template <>
+struct Kv8Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
   }
-}
+  __device__ __forceinline__ void floats(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+template <>
+struct Kv8Raw<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void floats(float* x) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
 __device__ __forceinline__ void kv8_store8(float* p, const float* x) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -77,8 +93,8 @@ __device__ __forceinline__ bool kv8_unit(const Kv8Geom& g, Kv8Unit& u) {
 // as 16-byte rows of the transposed plane (a partly written group byte by
 // byte: its other tokens' bytes are not this call's).
 template <typename T, int HD>
-__global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Geom g, const T* k, const T* v, long long ks,
-                                                                long long vs) {
+__global__ void __launch_bounds__(KV8_THREADS, (HD * sizeof(T) > 256 ? 12 : 16))
+    kv8_write_kernel(Kv8Geom g, const T* k, const T* v, long long ks, long long vs) {
   constexpr int HEADS = KV8_WRITE_HEADS;  // per block
   constexpr int LPV = HD / 8;             // lanes per vector
   constexpr int VPP = KV8_THREADS / LPV;  // vectors per pass
@@ -91,17 +107,16 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Geom g, const
   if (!kv8_unit(g, u)) return;
   const int head0 = blockIdx.y * HEADS, nh = min(HEADS, g.heads - head0);
   const int sub = threadIdx.x % LPV;
-  float x[PASSES][8];
+  Kv8Raw<T> raw[PASSES];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {  // all loads first: token by token, keys then values, head by head
     const int vec = threadIdx.x / LPV + i * VPP, h = vec % HEADS, t = vec / (2 * HEADS);
     const int pos = u.group * KV8_GROUP + t;
     if (pos >= u.t0 && pos < u.t1 && h < nh) {
       const size_t row = (size_t)(u.q.row0 + pos - u.q.pos0);
-      kv8_load8(((vec / HEADS) & 1 ? v + row * vs : k + row * ks) + (head0 + h) * HD + sub * 8, x[i]);
+      raw[i].load(((vec / HEADS) & 1 ? v + row * vs : k + row * ks) + (head0 + h) * HD + sub * 8);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+      raw[i].zero();
     }
   }
   u.page = kv8_checked(g, u.page);
@@ -111,16 +126,18 @@ __global__ void __launch_bounds__(KV8_THREADS) kv8_write_kernel(Kv8Geom g, const
     const int vec = threadIdx.x / LPV + i * VPP, h = vec % HEADS, kv = (vec / HEADS) & 1,
               t = vec / (2 * HEADS);
     // largest magnitude as bits: infinities and NaNs are above every number
+    float x[8];
+    raw[i].floats(x);
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
 #pragma unroll
     for (int o = LPV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bool nan = top >= 0x7F800000u;
     const int e2 = kv8_exponent(__uint_as_float(top));
     const float inv = kv8_pow2(-e2);
-    uint2 c = make_uint2(kv8_pack4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv),
-                         kv8_pack4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv));
+    uint2 c = make_uint2(kv8_pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                         kv8_pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
     if (nan) c = make_uint2(0, 0);
     const int pos = u.group * KV8_GROUP + t;
     if (kv)

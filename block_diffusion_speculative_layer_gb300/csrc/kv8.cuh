@@ -48,15 +48,19 @@ __device__ __forceinline__ bool kv8_seq(const Kv8Geom& g, int s, Kv8Seq& q) {
 // at most n / 16 + 2 aligned 16-token groups, so the units of two sequences
 // never meet and no block has to add up the sequences before its own.
 __host__ __device__ inline int kv8_units(int rows, int nseq) { return rows / KV8_GROUP + 2 * nseq; }
+// The unit's sequence (or -1): the last one whose units do not start behind
+// it, by a search over 32 sequences at a time.
 __device__ __forceinline__ int kv8_unit_seq(const Kv8Geom& g, int unit) {
   const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int i = 0; i < g.nseq; i += 32) {
-    const int s = i + lane;
-    const bool le = s < g.nseq && (g.row_start[s] >> 4) + 2 * s <= unit;
-    before += __popc(__ballot_sync(0xffffffffu, le));
+  int first = 0, n = g.nseq;  // it is among the n from `first` on, if any
+  for (;;) {
+    const int step = (n + 31) / 32, s = first + lane * step;
+    const bool le = lane * step < n && (g.row_start[s] >> 4) + 2 * s <= unit;
+    const int last = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+    if (last < 0 || step == 1) return first + last;
+    first += last * step;
+    n = min(step, n - last * step);
   }
-  return before - 1;
 }
 
 __device__ __forceinline__ size_t kv8_code_at(const Kv8Geom& g, int page, int kv, int head) {

@@ -500,3 +500,34 @@ def test_captured_step_replays_with_other_lengths(dfl):
     assert torch.equal(h.codes, h2.codes) and torch.equal(h.exps, h2.exps)
     dfl.kv8_check(h)
     dfl.kv8_check(h2)
+
+
+@pytest.mark.parametrize("rows,seqs,heads,group,hd", [(1, 39, 8, 2, 64), (640, 1, 8, 4, 64), (16, 20, 16, 4, 128)])
+def test_more_tiles_than_run_at_once(dfl, rows, seqs, heads, group, hd):
+    # the tiles behind the last full round are shared by two CTAs each; sequences share their pages
+    n = 4200
+    c = R.Case([(rows, n - rows - s) for s in range(seqs)], heads, hd, 64, seed=23, q_heads=heads * group)
+    c.table, c.n_pages = np.tile(np.arange(66, dtype=np.int32), (seqs, 1)), 66
+    cache = R.Cache(c)
+    cache.put_many(0, 0, c.vectors(n), c.vectors(n))
+    q = c.g.standard_normal((c.rows, heads * group, hd))
+    got, lse, x = attend(dfl, c, cache, q)
+    for j in np.unique(np.linspace(0, c.rows - 1, 24).astype(int)):   # these rows, every head
+        s = j // rows
+        one = R.Case([(1, int(c.positions(s)[j - s * rows]))], heads, hd, 64, q_heads=heads * group)
+        one.table, one.n_pages, cache.c = c.table, c.n_pages, one
+        compare(one, cache, got[[j]], lse[[j]], x[[j]])
+    assert np.isfinite(got).all() and np.isfinite(lse).all()
+
+
+def test_no_length_given_and_bounds_too_large(dfl):
+    # max_rows and max_len are bounds: far too large ones change nothing but the split
+    c = R.Case([(7, 300), (1, 0)], 2, 64, 32, seed=24, q_heads=6)
+    cache = filled(c)
+    h, table, start, lens = on_gpu(dfl, c, cache)
+    x = bf(c.g.standard_normal((c.rows, 6, 64))).view(c.rows, -1)
+    for max_rows, max_len in ((7, 0), (8, 307), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 40, 2 ** 40)):
+        for window in (0, 50, 2 ** 31 - 1):
+            out, lse = dfl.attention_kv8(x, h, table, start, lens, max_rows, max_len, window=window, lse=True)
+            dfl.kv8_check(h)
+            compare(c, cache, f64(out).reshape(c.rows, 6, 64), f64(lse), x, window=window)
