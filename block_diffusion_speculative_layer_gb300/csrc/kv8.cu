@@ -52,8 +52,11 @@ __device__ __forceinline__ void kv8_store8(__nv_bfloat16* p, const float* x) {
 // where it lies, which page) before the first of them.  A block takes a
 // 16-token group of one head (write) or two (read) and has all its loads in
 // flight at once.  Measured with 1, 2 and 4 heads to a block of 128 threads:
-// writing 8192 rows of 8 heads 15, 19 and 30 us, reading 16500 rows back 20,
-// 18 and 18 us (the bytes alone: 7.4 and 15 us).
+// writing 8192 rows of 8 heads 15, 19 and 30 us, reading 16500 rows back 21,
+// 18 and 18 us (the bytes alone: 7.4 and 15 us).  A writer that keeps its rows
+// as they lie until it uses them needs 32 registers (fp32 vectors of 128: 40):
+// 16 blocks to an SM, 13.2 us, with 10 of them 13.9.  A reader held to 12
+// blocks spills, 22 us.
 constexpr int KV8_THREADS = 128, KV8_WRITE_HEADS = 1, KV8_READ_HEADS = 2;
 
 // What a block works on: positions [t0, t1) of group `group` of sequence s,
