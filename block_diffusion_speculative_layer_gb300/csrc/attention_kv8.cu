@@ -67,7 +67,6 @@ struct Kv8Attn {
   int q_heads, group, max_rows, causal, window, tiles;
   unsigned solo;                // tiles that one CTA takes alone
   float scale_log2;
-  unsigned long long per_page;  // 2^32 / (groups of 16 tokens of a page), rounded up
 };
 
 constexpr int K8_CHUNK = 128;     // keys per chunk: one per tensor-memory lane
@@ -486,9 +485,8 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   for (int i = 0; i < STAGES; ++i) {
     early[i] = -1;
     if (warp > ISSUER && lane < 8 && a.window == 0) {
-      const unsigned entry =
-          (unsigned)(((unsigned long long)((unsigned)(rank + i * C) * (K8_CHUNK / 16) + lane) * a.per_page) >> 32);
-      if (entry < (unsigned)g.pt_stride) early[i] = g.page_table[(size_t)s * g.pt_stride + entry];
+      const int entry = kv8_entry(g, (rank + i * C) * (K8_CHUNK / 16) + lane);
+      if (entry < g.pt_stride) early[i] = g.page_table[(size_t)s * g.pt_stride + entry];
     }
   }
 
@@ -535,7 +533,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
     Place p{-2, 0};
     if (i < n_mine && lane < 8) {
       const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + lane;
-      const unsigned entry = (unsigned)(((unsigned long long)group * a.per_page) >> 32);  // group / groups of a page
+      const int entry = kv8_entry(g, (int)group);
       p.slot = (int)(group * 16 - entry * g.page_tokens);
       if ((int)group * 16 < len)
         p.page = known != 0x7fffffff ? known : g.page_table[(size_t)s * g.pt_stride + entry];
@@ -1114,7 +1112,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
                               int32_t causal, int32_t window, int32_t cluster_ctas, int32_t* err_dev, void* stream) {
   Kv8Attn a{};
   a.g = Kv8Geom{(uint8_t*)codes_dev, (uint8_t*)exps_dev, page_table_dev, row_start_dev, kv_len_dev, err_dev,
-                n_pages, page_tokens, n_kv_heads, head_dim, pt_stride, nseq, rows};
+                n_pages, page_tokens, n_kv_heads, head_dim, pt_stride, nseq, rows, 0};
   if (rows < 0 || nseq < 0 || nseq > (1 << 20) || max_rows < 0 || max_len < 0 || (causal != 0 && causal != 1) ||
       window < 0 || (window > 0 && !causal) || !isfinite(scale))
     return DF_EINVAL;
@@ -1138,8 +1136,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   a.max_rows = max_rows < rows ? max_rows : rows;
   a.causal = causal;
   a.window = window;
-  // exact for a group number below 2^26 and at most 64 groups to a page
-  a.per_page = ((1ull << 32) + page_tokens / 16 - 1) / (page_tokens / 16);
+  a.g.per_page = kv8_per_page(page_tokens);
   a.scale_log2 = (float)(scale * (1.4426950408889634 / K8_QSCALE));
   // The narrowest tile that holds a sequence's rows; more than 64 rows are cut
   // into tiles of 64 or 128.  A sequence's tiles are at most so many, and of

@@ -16,6 +16,19 @@ struct Kv8Raw<float> {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
+  // bits of the largest magnitude in the vector, which LPV lanes hold:
+  // infinities and NaNs are above every number
+  template <int LPV>
+  __device__ __forceinline__ uint32_t largest() const {
+    float x[8];
+    floats(x);
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = LPV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top;
+  }
   __device__ __forceinline__ void floats(float* x) const {
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
   }
@@ -25,6 +38,13 @@ struct Kv8Raw<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  template <int LPV>
+  __device__ __forceinline__ uint32_t largest() const {  // two at a time
+    uint32_t top = __vmaxu2(__vmaxu2(a.x & 0x7FFF7FFFu, a.y & 0x7FFF7FFFu), __vmaxu2(a.z & 0x7FFF7FFFu, a.w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int o = LPV / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return max(top & 0xFFFF0000u, top << 16);
+  }
   __device__ __forceinline__ void floats(float* x) const {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -52,11 +72,13 @@ __device__ __forceinline__ void kv8_store8(__nv_bfloat16* p, const float* x) {
 // where it lies, which page) before the first of them.  A block takes a
 // 16-token group of one head (write) or two (read) and has all its loads in
 // flight at once.  Measured with 1, 2 and 4 heads to a block of 128 threads:
-// writing 8192 rows of 8 heads 15, 19 and 30 us, reading 16500 rows back 21,
-// 18 and 18 us (the bytes alone: 7.4 and 15 us).  A writer that keeps its rows
-// as they lie until it uses them needs 32 registers (fp32 vectors of 128: 40):
-// 16 blocks to an SM, 13.2 us, with 10 of them 13.9.  A reader held to 12
-// blocks spills, 22 us.
+// writing 8192 rows of 8 heads 11.0, 11.0 and 12.2 us and 32 rows 3.5, 4.1 and
+// 5.1, reading 16500 rows back 21, 18 and 18 us (the bytes alone: 7.4 and 15
+// us).  A writer that keeps its rows as they lie until it uses them needs 32
+// registers (fp32 vectors of 128: 40), which allows 16 blocks to an SM; most
+// of its time is instructions (issue slots 75% busy at 13.2 us, before maxima
+// were taken two at a time and addresses once for all rows).  A reader held
+// to 12 blocks spills, 22 us.
 constexpr int KV8_THREADS = 128, KV8_WRITE_HEADS = 1, KV8_READ_HEADS = 2;
 
 // What a block works on: positions [t0, t1) of group `group` of sequence s,
@@ -86,8 +108,9 @@ __device__ __forceinline__ bool kv8_unit(const Kv8Geom& g, Kv8Unit& u) {
   if (u.t0 >= u.t1) return false;
   // a group before position 0 is padding: it has no page (KV8_PADDING); the
   // look-up is checked by kv8_checked, after the loads that do not need it
-  u.page = u.group >= 0 ? g.page_table[(size_t)u.s * g.pt_stride + u.group * KV8_GROUP / g.page_tokens] : KV8_PADDING;
-  u.slot0 = u.group >= 0 ? (u.group * KV8_GROUP) % g.page_tokens : 0;
+  const int entry = u.group >= 0 ? kv8_entry(g, u.group) : 0;
+  u.page = u.group >= 0 ? g.page_table[(size_t)u.s * g.pt_stride + entry] : KV8_PADDING;
+  u.slot0 = u.group >= 0 ? u.group * KV8_GROUP - entry * g.page_tokens : 0;
   return true;
 }
 
@@ -109,45 +132,40 @@ __global__ void __launch_bounds__(KV8_THREADS, (HD * sizeof(T) > 256 ? 12 : 16))
   Kv8Unit u;
   if (!kv8_unit(g, u)) return;
   const int head0 = blockIdx.y * HEADS, nh = min(HEADS, g.heads - head0);
-  const int sub = threadIdx.x % LPV;
+  // this lane's vectors: keys or values of one head, tokens t, t + STEP, ...
+  constexpr int STEP = VPP / (2 * HEADS);
+  static_assert(VPP % (2 * HEADS) == 0, "a thread's vectors are of one head and kind");
+  const int sub = threadIdx.x % LPV, vec = threadIdx.x / LPV;
+  const int h = vec % HEADS, kv = vec / HEADS & 1, t = vec / (2 * HEADS), pos = u.group * KV8_GROUP + t;
+  const long long stride = kv ? vs : ks;
+  const T* src = (kv ? v : k) + (u.q.row0 + pos - u.q.pos0) * stride + (head0 + h) * HD + sub * 8;
   Kv8Raw<T> raw[PASSES];
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {  // all loads first: token by token, keys then values, head by head
-    const int vec = threadIdx.x / LPV + i * VPP, h = vec % HEADS, t = vec / (2 * HEADS);
-    const int pos = u.group * KV8_GROUP + t;
-    if (pos >= u.t0 && pos < u.t1 && h < nh) {
-      const size_t row = (size_t)(u.q.row0 + pos - u.q.pos0);
-      raw[i].load(((vec / HEADS) & 1 ? v + row * vs : k + row * ks) + (head0 + h) * HD + sub * 8);
-    } else {
+  for (int i = 0; i < PASSES; ++i) {  // all loads first
+    if (pos + i * STEP >= u.t0 && pos + i * STEP < u.t1 && h < nh)
+      raw[i].load(src + i * STEP * stride);
+    else
       raw[i].zero();
-    }
   }
   u.page = kv8_checked(g, u.page);
   if (u.page < 0) return;
+  uint8_t* keys = g.codes + kv8_code_at(g, u.page, 0, head0 + h) + (size_t)(u.slot0 + t) * HD + sub * 8;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
-    const int vec = threadIdx.x / LPV + i * VPP, h = vec % HEADS, kv = (vec / HEADS) & 1,
-              t = vec / (2 * HEADS);
-    // largest magnitude as bits: infinities and NaNs are above every number
-    float x[8];
-    raw[i].floats(x);
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = LPV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t top = raw[i].template largest<LPV>();
     const bool nan = top >= 0x7F800000u;
     const int e2 = kv8_exponent(__uint_as_float(top));
     const float inv = kv8_pow2(-e2);
+    float x[8];
+    raw[i].floats(x);
     uint2 c = make_uint2(kv8_pack4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
                          kv8_pack4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
     if (nan) c = make_uint2(0, 0);
-    const int pos = u.group * KV8_GROUP + t;
     if (kv)
-      *reinterpret_cast<uint2*>(&sV[h][t][sub * 8]) = c;
-    else if (pos >= u.t0 && pos < u.t1 && h < nh)
-      *reinterpret_cast<uint2*>(g.codes + kv8_code_at(g, u.page, 0, head0 + h) + (size_t)(u.slot0 + t) * HD + sub * 8) = c;
-    if (sub == 0) sE[h][t][kv] = (uint8_t)(nan ? KV8_NAN : e2 + KV8_BIAS);
+      *reinterpret_cast<uint2*>(&sV[h][t + i * STEP][sub * 8]) = c;
+    else if (pos + i * STEP >= u.t0 && pos + i * STEP < u.t1 && h < nh)
+      *reinterpret_cast<uint2*>(keys + i * STEP * HD) = c;
+    if (sub == 0) sE[h][t + i * STEP][kv] = (uint8_t)(nan ? KV8_NAN : e2 + KV8_BIAS);
   }
   __syncthreads();
   const int lo = max(u.t0, 0) - u.group * KV8_GROUP, hi = u.t1 - u.group * KV8_GROUP;
@@ -165,10 +183,10 @@ __global__ void __launch_bounds__(KV8_THREADS, (HD * sizeof(T) > 256 ? 12 : 16))
       for (int t = lo; t < hi; ++t) dst[t] = sV[h][t][d];
     }
   }
-  const int h = threadIdx.x / KV8_GROUP, t = threadIdx.x % KV8_GROUP;
-  if (h < nh && t >= lo && t < hi)
-    *reinterpret_cast<uint16_t*>(g.exps + kv8_exp_at(g, u.page, head0 + h, u.slot0 + t)) =
-        (uint16_t)(sE[h][t][0] | ((uint32_t)sE[h][t][1] << 8));
+  const int eh = threadIdx.x / KV8_GROUP, et = threadIdx.x % KV8_GROUP;
+  if (eh < nh && et >= lo && et < hi)
+    *reinterpret_cast<uint16_t*>(g.exps + kv8_exp_at(g, u.page, head0 + eh, u.slot0 + et)) =
+        (uint16_t)(sE[eh][et][0] | ((uint32_t)sE[eh][et][1] << 8));
 }
 
 // Read: the same, the other way.  The value plane is transposed through
@@ -265,14 +283,15 @@ df_status df_op_kv8_write(const void* k_dev, const void* v_dev, int32_t dtype, i
                           int32_t n_kv_heads, int32_t head_dim, const int32_t* page_table_dev, int32_t pt_stride,
                           const int32_t* row_start_dev, const int32_t* kv_len_dev, int32_t nseq, int32_t* err_dev,
                           void* stream) {
-  const Kv8Geom g{(uint8_t*)codes_dev, (uint8_t*)exps_dev, page_table_dev, row_start_dev, kv_len_dev, err_dev,
-                  n_pages, page_tokens, n_kv_heads, head_dim, pt_stride, nseq, rows};
+  Kv8Geom g{(uint8_t*)codes_dev, (uint8_t*)exps_dev, page_table_dev, row_start_dev, kv_len_dev, err_dev,
+                  n_pages, page_tokens, n_kv_heads, head_dim, pt_stride, nseq, rows, 0};
   if ((dtype != DF_FP32 && dtype != DF_BF16) || rows < 0 || nseq < 0 || nseq > (1 << 20)) return DF_EINVAL;
   if (rows == 0 || nseq == 0) return DF_OK;
   if (!k_dev || !v_dev || !kv8_geom_ok(g) || !kv8_aligned(k_dev, 16) || !kv8_aligned(v_dev, 16)) return DF_EINVAL;
   const int per16 = dtype == DF_FP32 ? 4 : 8;  // elements in 16 bytes
   const long long width = (long long)n_kv_heads * head_dim;
   if (k_stride < width || v_stride < width || k_stride % per16 || v_stride % per16) return DF_EINVAL;
+  g.per_page = kv8_per_page(page_tokens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DF_FP32 ? launch_kv8_write<float>(g, k_dev, v_dev, k_stride, v_stride, st)
                                          : launch_kv8_write<__nv_bfloat16>(g, k_dev, v_dev, k_stride, v_stride, st);
@@ -283,11 +302,12 @@ df_status df_op_kv8_read(const void* codes_dev, const void* exps_dev, int32_t n_
                          int32_t n_kv_heads, int32_t head_dim, const int32_t* page_table_dev, int32_t pt_stride,
                          const int32_t* row_start_dev, const int32_t* kv_len_dev, int32_t nseq, int32_t rows,
                          int32_t dtype, void* k_dev, void* v_dev, int32_t* err_dev, void* stream) {
-  const Kv8Geom g{(uint8_t*)codes_dev, (uint8_t*)exps_dev, page_table_dev, row_start_dev, kv_len_dev, err_dev,
-                  n_pages, page_tokens, n_kv_heads, head_dim, pt_stride, nseq, rows};
+  Kv8Geom g{(uint8_t*)codes_dev, (uint8_t*)exps_dev, page_table_dev, row_start_dev, kv_len_dev, err_dev,
+                  n_pages, page_tokens, n_kv_heads, head_dim, pt_stride, nseq, rows, 0};
   if ((dtype != DF_FP32 && dtype != DF_BF16) || rows < 0 || nseq < 0 || nseq > (1 << 20)) return DF_EINVAL;
   if (rows == 0 || nseq == 0) return DF_OK;
   if (!k_dev || !v_dev || !kv8_geom_ok(g) || !kv8_aligned(k_dev, 16) || !kv8_aligned(v_dev, 16)) return DF_EINVAL;
+  g.per_page = kv8_per_page(page_tokens);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = dtype == DF_FP32 ? launch_kv8_read<float>(g, k_dev, v_dev, st)
                                          : launch_kv8_read<__nv_bfloat16>(g, k_dev, v_dev, st);

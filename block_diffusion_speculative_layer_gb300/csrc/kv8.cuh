@@ -24,12 +24,22 @@ struct Kv8Geom {
   const int* kv_len;
   int* err;
   int n_pages, page_tokens, heads, hd, pt_stride, nseq, rows;
+  unsigned long long per_page;  // 2^32 / (groups of 16 tokens of a page), rounded up
 };
 
 constexpr int KV8_GROUP = 16;  // tokens whose values lie together, transposed
 constexpr int KV8_NAN = 255;   // exponent byte of a vector that holds no numbers
 constexpr int KV8_BIAS = 127;
 constexpr int KV8_EMIN = -100, KV8_EMAX = 119;  // keeps c * 2^e finite and normal in bf16 and fp32
+
+// The page-table entry of a sequence's 16-token group: exact for a group below
+// 2^26 and at most 64 groups to a page.
+inline unsigned long long kv8_per_page(int page_tokens) {
+  return ((1ull << 32) + page_tokens / KV8_GROUP - 1) / (page_tokens / KV8_GROUP);
+}
+__device__ __forceinline__ int kv8_entry(const Kv8Geom& g, int group) {
+  return (int)(((unsigned long long)(unsigned)group * g.per_page) >> 32);
+}
 
 // One sequence's rows: first row, number of rows, position of the first.
 struct Kv8Seq {
