@@ -583,9 +583,11 @@ df_status df_op_kv8_read(const void* codes_dev, const void* exps_dev, int32_t n_
  *                   sets error bit 2)
  *   max_len         bound on kv_len, used to choose the split alone
  *   cluster_ctas    CTAs that share one tile's keys: 1, 2, 4, 8 or 16, or 0
- *                   for a choice by the sizes.  The split decides the order of
- *                   summation: a row's bits depend on its own query and keys
- *                   and on this number, not on the other rows of the call.
+ *                   for a choice by the sizes of the call (and, in a call of
+ *                   more tiles than the GPU runs at once, by the tile's
+ *                   place).  The split decides the order of summation: with a
+ *                   number given, a row's bits depend on its own query and
+ *                   keys and on this number, not on the other rows of the call.
  * A row that sees nothing gives zeros and lse -inf; a row that sees a vector
  * without numbers (byte 255) gives NaN. */
 df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev, int64_t out_stride, float* lse_dev,
