@@ -518,7 +518,10 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   const int pos_first = sq.pos0 + j0, pos_last = sq.pos0 + token(nr - 1);
   const int full_lo = lowest(pos_last), full_hi = highest(pos_first), end = highest(pos_last) + 1;
   const int c_end = (end + K8_CHUNK - 1) / K8_CHUNK;
-  int c_first = min(lowest(pos_first), len) / K8_CHUNK;
+  // positions [begin, end) are what the tile sees: pages of others are not
+  // looked at (a window may have left them), bytes of others count as zeros
+  const int begin = min(lowest(pos_first), len);
+  int c_first = begin / K8_CHUNK;
   c_first += (rank - c_first) & (C - 1);
   const unsigned n_mine = c_end > c_first ? (unsigned)(c_end - c_first + C - 1) >> lg : 0;
 
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
       const unsigned group = (unsigned)(c_first + (int)i * C) * (K8_CHUNK / 16) + lane;
       const int entry = kv8_entry(g, (int)group);
       p.slot = (int)(group * 16 - entry * g.page_tokens);
-      if ((int)group * 16 < len)
+      if ((int)group * 16 < end && (int)group * 16 + 16 > begin)
         p.page = known != 0x7fffffff ? known : g.page_table[(size_t)s * g.pt_stride + entry];
     }
     return p;
@@ -777,14 +780,15 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
         uint4 v[VSHARE];
 #pragma unroll
         for (int q = 0; q < VSHARE; ++q) v[q] = k8_lds16(row + q * 16 * HD);
-        if (live != 0xff || key0 + K8_CHUNK > len) {  // bytes behind the last position may be anything: zeros
+        if (live != 0xff || key0 < begin || key0 + K8_CHUNK > end) {  // bytes outside may be anything: zeros
 #pragma unroll
           for (int q = 0; q < VSHARE; ++q) {
-            const int gr = v0 + q, n = (live >> gr) & 1 ? len - key0 - gr * 16 : 0;
-            v[q].x = n >= 4 ? v[q].x : n <= 0 ? 0u : v[q].x & ((1u << (8 * n)) - 1);
-            v[q].y = n >= 8 ? v[q].y : n <= 4 ? 0u : v[q].y & ((1u << (8 * (n - 4))) - 1);
-            v[q].z = n >= 12 ? v[q].z : n <= 8 ? 0u : v[q].z & ((1u << (8 * (n - 8))) - 1);
-            v[q].w = n >= 16 ? v[q].w : n <= 12 ? 0u : v[q].w & ((1u << (8 * (n - 12))) - 1);
+            const int gr = v0 + q, n = (live >> gr) & 1 ? end - key0 - gr * 16 : 0, m = begin - key0 - gr * 16;
+            auto first = [](int k) { return k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1; };  // k bytes
+            v[q].x &= first(n) & ~first(m);
+            v[q].y &= first(n - 4) & ~first(m - 4);
+            v[q].z &= first(n - 8) & ~first(m - 8);
+            v[q].w &= first(n - 12) & ~first(m - 12);
           }
         }
 #pragma unroll

@@ -538,7 +538,9 @@ df_status df_op_accept_sampled(const int32_t* drafts_dev, const float* q_logits_
  * other lengths.  A sequence whose entries are out of range (row_start, or a
  * kv_len outside [0, pt_stride * page_tokens]) is left out, and a page id
  * outside [0, n_pages) makes its positions unwritten, zero when read and
- * invisible to attention; both set bit 2 of err_dev.
+ * invisible to attention; both set bit 2 of err_dev.  Attention does not look
+ * at pages none of whose positions a row sees (those a sliding window has
+ * left may be given to others), nor at what unseen positions hold.
  *
  * Every call is stream-ordered, allocates nothing, keeps nothing between
  * calls, does not synchronise and can be captured.  err_dev (may be NULL): a

@@ -531,3 +531,27 @@ def test_no_length_given_and_bounds_too_large(dfl):
             out, lse = dfl.attention_kv8(x, h, table, start, lens, max_rows, max_len, window=window, lse=True)
             dfl.kv8_check(h)
             compare(c, cache, f64(out).reshape(c.rows, 6, 64), f64(lse), x, window=window)
+
+
+@pytest.mark.parametrize("hd,page,rows", [(128, 16, 1), (128, 16, 5), (64, 32, 40), (128, 64, 70)])
+def test_pages_that_a_window_has_left(dfl, hd, page, rows):
+    # no page id, or bytes that are no numbers, at every position that no row sees
+    window, n = 77, 900
+    c = R.Case([(rows, n - rows), (1, 30)], 2, hd, page, seed=25, q_heads=8)
+    cache = R.Cache(c)
+    cache.codes[:] = 0x7F                                   # NaN codes
+    cache.exps[:] = 255
+    first = n - rows - window + 1                           # the first position that a row sees
+    k, v = c.vectors(n), c.vectors(n)
+    cache.put_many(0, first, k[first:], v[first:])
+    cache.put_many(1, 0, c.vectors(31), c.vectors(31))
+    q = c.g.standard_normal((c.rows, 8, hd))
+    whole = c.table.copy()
+    c.table[0, :first // page] = -1
+    got, lse, x = attend(dfl, c, cache, q, window=window)   # kv8_check: nothing was flagged
+    c.table = whole
+    cache.put_many(0, 0, k, v)
+    compare(c, cache, got, lse, x, window=window)
+    want, wlse, _ = attend(dfl, c, cache, q, window=window)
+    np.testing.assert_array_equal(got, want)
+    np.testing.assert_array_equal(lse, wlse)
