@@ -600,7 +600,11 @@ def kv8_cache(n_pages: int, n_kv_heads: int, head_dim: int = 128, page_tokens: i
 
 def kv8_check(cache: KV8Cache):
     """Raise if a call on this cache met a page id or length out of range
-    (or a wait that ran out), and clear its error word.  Synchronises."""
+    (or a wait that ran out), and clear its error word.  Waits for every
+    stream of the cache's device."""
+    import torch
+    if cache.err.is_cuda:
+        torch.cuda.synchronize(cache.err.device)
     e = int(cache.err.item())
     cache.err.zero_()
     if e:

@@ -555,3 +555,18 @@ def test_pages_that_a_window_has_left(dfl, hd, page, rows):
     want, wlse, _ = attend(dfl, c, cache, q, window=window)
     np.testing.assert_array_equal(got, want)
     np.testing.assert_array_equal(lse, wlse)
+
+
+def test_check_waits_for_other_streams(dfl):
+    c = R.Case([(4, 60)], 2, 64, 16, seed=26)
+    c.table[0, 0] = c.n_pages
+    h, table, start, lens = on_gpu(dfl, c, R.Cache(c))
+    q = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)   # about 10 ms
+        dfl.attention_kv8(q, h, table, start, lens, 4, 64, out=torch.empty_like(q))
+    with pytest.raises(dfl.DfError):
+        dfl.kv8_check(h)
+    dfl.kv8_check(h)
