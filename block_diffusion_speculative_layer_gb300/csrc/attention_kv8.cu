@@ -53,6 +53,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <iterator>
 
 #include "kv8.cuh"
 
@@ -66,6 +67,7 @@ struct Kv8Attn {
   long long qs, os;  // row strides (elements)
   int q_heads, group, max_rows, causal, window, tiles;
   unsigned solo;                // tiles that one CTA takes alone
+  unsigned long long per_cluster;  // 2^32 / (CTAs of a cluster), rounded up
   float scale_log2;
 };
 
@@ -443,8 +445,8 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   // Of a causal sequence's tiles the last, which sees the most, starts first.
   const bool alone = blockIdx.x < a.solo;
   const int C = alone ? 1 : (int)k8_cluster_size(), rank = alone ? 0 : (int)k8_rank();
-  const int lg = 31 - __clz(C);  // clusters are powers of two
-  const unsigned unit = alone ? blockIdx.x : a.solo + ((blockIdx.x - a.solo) >> lg);
+  auto over_c = [&](unsigned x) { return alone ? x : (unsigned)(((unsigned long long)x * a.per_cluster) >> 32); };
+  const unsigned unit = alone ? blockIdx.x : a.solo + over_c(blockIdx.x - a.solo);
   const int head = (int)(unit / (unsigned)(a.tiles * g.nseq)), in_head = (int)unit - head * a.tiles * g.nseq;
   const int s = in_head / a.tiles, nth = in_head - s * a.tiles;
   const int tile = a.causal && a.window == 0 ? a.tiles - 1 - nth : nth;
@@ -522,8 +524,9 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
   // looked at (a window may have left them), bytes of others count as zeros
   const int begin = min(lowest(pos_first), len);
   int c_first = begin / K8_CHUNK;
-  c_first += (rank - c_first) & (C - 1);
-  const unsigned n_mine = c_end > c_first ? (unsigned)(c_end - c_first + C - 1) >> lg : 0;
+  const int from = c_first - (int)over_c(c_first) * C;  // the first chunk's rank
+  c_first += rank - from + (rank < from ? C : 0);
+  const unsigned n_mine = c_end > c_first ? over_c(c_end - c_first + C - 1) : 0;
 
   bool ok = true;
   // Staging: a chunk's 8 groups of 16 keys, of values and of exponents are 24
@@ -1010,9 +1013,11 @@ __global__ void __launch_bounds__(K8<HD, N>::THREADS, K8<HD, N>::PER_SM)
         if (q < C) add(x[q], q);
       if (C > 8) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = k8_remote_f4(k8_remote(part, 8 + q));
+        for (int q = 0; q < 8; ++q)
+          if (8 + q < C) x[q] = k8_remote_f4(k8_remote(part, 8 + q));
 #pragma unroll
-        for (int q = 0; q < 8; ++q) add(x[q], 8 + q);
+        for (int q = 0; q < 8; ++q)
+          if (8 + q < C) add(x[q], 8 + q);
       }
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const long long at = s_tok[row];
@@ -1081,22 +1086,24 @@ static cudaError_t k8_launch(const Kv8Attn& a, const CUtensorMap& map, int clust
 // measured with 8 to 256 tiles of 3 to 257 chunks: what a CTA takes for a chunk
 // and for the rest, what joining the parts adds, and what CTAs cost one another
 // (a second on an SM; with c = 1 from fewer).  More clusters than run at once
-// cost a second round (that depends on how the SMs are grouped: 16 tiles, 2048
-// positions, 16 rows: 15 us with 4 or 8 CTAs to a tile, 25 with 16).  Estimate
-// and time of 16 rows of 4 heads, c = 1, 4, 8: one sequence at 512, 8 tiles,
-// 12.1 11.1 10.1 and 12.1 10.9 10.0; two at 1024, 16.3 12.2 13.3 and 16.5 12.2
-// 14.1; four at 8192, 75 35 28 and 77 35 27.  Tiles of 64 and 128, c = 1: 32
-// rows of one sequence at 1024, 16.3 20.7 and 16.8 20.8; 64 rows of eight at
-// 8192, 111 94 and 108 98.
+// cost a second round (that depends on how the SMs are grouped: 16 tiles of 64
+// rows, 2048 positions: 15 us with 4 or 8 CTAs to a tile, 25 with 16), and sizes
+// between the powers of two fill more SMs (23 tiles of 128 rows, 6000
+// positions: 24 us with 6, 29 with 4, 41 with 8).  Estimate and time of 16 rows
+// of 4 heads, c = 1, 4, 8: one sequence at 512, 8 tiles, 12.1 11.1 10.1 and
+// 12.1 10.9 10.0; two at 1024, 16.3 12.2 13.3 and 16.5 12.2 14.1; four at
+// 8192, 75 35 26 and 77 35 27.  Tiles of 64 and 128, c = 1: 32 rows of one
+// sequence at 1024, 16.3 20.7 and 16.8 20.8; 64 rows of eight at 8192, 111 94
+// and 108 98.
 static float k8_time(int n, int c, long long work, long long chunks) {
-  constexpr int fit[2][5] = {{304, 152, 74, 36, 14}, {152, 76, 36, 15, 7}};  // clusters at once
+  constexpr int fit[2][8] = {{304, 152, 96, 74, 46, 35, 22, 14}, {152, 76, 46, 36, 23, 15, 8, 7}};  // clusters at once
   constexpr float chunk[4] = {0.66f, 0.8f, 1.05f, 1.3f}, rest[4] = {4.7f, 5.4f, 6.8f, 9.f},
                   join[4] = {1.3f, 1.6f, 2.2f, 3.2f};
   const int i = n == 16 ? 0 : n == 32 ? 1 : n == 64 ? 2 : 3;
-  const int j = c == 1 ? 0 : c == 2 ? 1 : c == 4 ? 2 : c == 8 ? 3 : 4;
+  const int j = c <= 4 ? c - 1 : c == 6 ? 4 : c == 8 ? 5 : c == 12 ? 6 : 7;
   const long long ctas = work * c, rounds = (work + fit[i == 3][j] - 1) / fit[i == 3][j];
   const bool shared = i < 3 && ctas > K8_SMS, busy = i < 3 && ctas > K8_SMS / 2;
-  const float slower = shared ? (c == 1 ? 1.5f : 1.8f) : busy ? 1.4f : i < 3 && c == 1 && ctas > K8_SMS / 4 ? 1.2f : 1.f;
+  const float slower = shared ? (c == 1 ? 1.5f : 1.6f) : busy ? 1.4f : i < 3 && c == 1 && ctas > K8_SMS / 4 ? 1.2f : 1.f;
   const float fixed = rest[i] + (c == 1 ? 0.f : c == 2 || c == 16 ? 1.4f * join[i] : join[i]);
   return (float)rounds *
          (fixed * (shared ? 1.25f : busy ? 1.15f : 1.f) + (float)((chunks + c - 1) / c) * chunk[i] * slower);
@@ -1120,9 +1127,8 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   if (rows < 0 || nseq < 0 || nseq > (1 << 20) || max_rows < 0 || max_len < 0 || (causal != 0 && causal != 1) ||
       window < 0 || (window > 0 && !causal) || !isfinite(scale))
     return DF_EINVAL;
-  if (cluster_ctas != 0 && cluster_ctas != 1 && cluster_ctas != 2 && cluster_ctas != 4 && cluster_ctas != 8 &&
-      cluster_ctas != 16)
-    return DF_EINVAL;
+  constexpr int sizes[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  if (cluster_ctas && std::find(std::begin(sizes), std::end(sizes), cluster_ctas) == std::end(sizes)) return DF_EINVAL;
   if (rows == 0 || nseq == 0 || max_rows == 0) return DF_OK;
   if (!q_dev || !out_dev || !kv8_geom_ok(a.g) || !kv8_aligned(q_dev, 16) || !kv8_aligned(out_dev, 16) ||
       !kv8_aligned(lse_dev, 4))
@@ -1155,8 +1161,8 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
   int n = wanted <= 16 ? 16 : wanted <= 32 ? 32 : 64, cluster = 1;
   float best = INFINITY;
   for (int m = n; m <= (wanted > 64 ? 128 : n); m *= 2)
-    for (int c = cluster_ctas ? cluster_ctas : 1; c <= (cluster_ctas ? cluster_ctas : 16); c *= 2) {
-      if (!cluster_ctas && c / 2 >= std::max(chunks_of(m), 1ll)) break;
+    for (const int c : sizes) {
+      if (cluster_ctas ? c != cluster_ctas : c > 1 && c / 2 >= chunks_of(m)) continue;
       const float t = k8_time(m, c, work_of(m), chunks_of(m));
       if (t < best) best = t, n = m, cluster = c;
     }
@@ -1173,6 +1179,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
     cluster = 2;
     a.solo = (unsigned)(all_of(n) / room * room);
   }
+  a.per_cluster = ((1ull << 32) + cluster - 1) / cluster;  // exact: 3, 6 and 12 have few CTAs and chunks
   CUtensorMap map;
   if (!k8_tmap(&map, a.g)) return DF_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -584,8 +584,8 @@ df_status df_op_kv8_read(const void* codes_dev, const void* exps_dev, int32_t n_
  *   max_rows        bound on one sequence's rows (a longer one is left out and
  *                   sets error bit 2)
  *   max_len         bound on kv_len, used to choose the split alone
- *   cluster_ctas    CTAs that share one tile's keys: 1, 2, 4, 8 or 16, or 0
- *                   for a choice by the sizes of the call (and, in a call of
+ *   cluster_ctas    CTAs that share one tile's keys: 1, 2, 3, 4, 6, 8, 12
+ *                   or 16, or 0 for a choice by the sizes (and, in a call of
  *                   more tiles than the GPU runs at once, by the tile's
  *                   place).  The split decides the order of summation: with a
  *                   number given, a row's bits depend on its own query and

@@ -570,3 +570,13 @@ def test_check_waits_for_other_streams(dfl):
     with pytest.raises(dfl.DfError):
         dfl.kv8_check(h)
     dfl.kv8_check(h)
+
+
+@pytest.mark.parametrize("cluster", [3, 6, 12])
+def test_splits_that_are_no_power_of_two(dfl, cluster):
+    c = R.Case([(16, 900), (1, 3), (2, 4000), (40, 130)], 2, 128, 16, seed=27, q_heads=8)
+    cache = filled(c)
+    q = c.g.standard_normal((c.rows, 8, 128))
+    for window in (0, 700):
+        got, lse, x = attend(dfl, c, cache, q, window=window, cluster_ctas=cluster)
+        compare(c, cache, got, lse, x, window=window)
