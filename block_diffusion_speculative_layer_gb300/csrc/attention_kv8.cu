@@ -1167,7 +1167,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
       if (t < best) best = t, n = m, cluster = c;
     }
   const long long tiles = (wanted + n - 1) / n;
-  if (all_of(n) > 0x7fffffff / 16) return DF_EINVAL;
+  if (all_of(n) > (1 << 29) / 16) return DF_EINVAL;
   a.tiles = (int)tiles;
   // Tiles that fill the GPU several times, and half of it or less at the end:
   // those last ones are shared by two CTAs each (2048 rows at 6144, 512 tiles:
@@ -1179,7 +1179,7 @@ df_status df_op_attention_kv8(const void* q_dev, int64_t q_stride, void* out_dev
     cluster = 2;
     a.solo = (unsigned)(all_of(n) / room * room);
   }
-  a.per_cluster = ((1ull << 32) + cluster - 1) / cluster;  // exact: 3, 6 and 12 have few CTAs and chunks
+  a.per_cluster = ((1ull << 32) + cluster - 1) / cluster;  // exact for CTAs below 2^29
   CUtensorMap map;
   if (!k8_tmap(&map, a.g)) return DF_ECUDA;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

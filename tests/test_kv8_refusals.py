@@ -72,7 +72,7 @@ def test_bad_attention(dfl):
     for bad in (dict(q=None), dict(out=None), dict(hq=36), dict(hq=4), dict(hq=0), dict(qs=4088), dict(os=4092),
                 dict(qs=4100), dict(q=P(0x1008)), dict(out=P(0x1002)), dict(lse=P(0x1002)), dict(max_rows=-1),
                 dict(max_len=-1), dict(causal=2), dict(window=-1), dict(window=5, causal=0), dict(scale=math.nan),
-                dict(scale=math.inf), dict(cla=3), dict(cla=32), dict(cla=-1), dict(nseq=1 << 21)):
+                dict(scale=math.inf), dict(cla=5), dict(cla=32), dict(cla=-1), dict(nseq=1 << 21)):
         assert attend(dfl, **bad) == dfl.DF_EINVAL, bad
     assert attend(dfl, max_rows=0) == dfl.DF_OK
 
@@ -114,3 +114,9 @@ def test_plain_exponents():
     assert e(0.0) == -100 and e(3e38) == 119 and e(1e-40) == -100
     codes, b = R.quantise(np.array([1.0, np.inf]))
     assert b == 255 and (codes == 0).all()
+
+
+def test_attention_refuses_more_tiles_than_a_launch_counts(dfl):
+    # 2^20 sequences of up to 2^20 rows and 8 heads of 4: far above 2^25 tiles
+    for cla in (0, 12, 16):
+        assert attend(dfl, nseq=1 << 20, rows=1 << 20, max_rows=1 << 20, cla=cla) == dfl.DF_EINVAL
